@@ -225,6 +225,83 @@ moe_status_t moe_forward_w8_timed(const moe_bf16_t* x, const float* logits, cons
 /* 1 if moe_forward_w8 accepts `shape` (the one-launch layer's shapes), else 0. */
 int moe_forward_w8_supported(moe_shape_t shape);
 
+/* Microscaled (MX) operands: 32 consecutive elements of a row form a block with
+ * one E8M0 scale byte, code c = the power of two 2^(c - 127), 255 = NaN.  Elements are
+ * E2M1 (sign, 2 exponent bits with bias 1, 1 significand bit: 0 .5 1 1.5 2 3 4 6), two
+ * to a byte with the lower column in the low nibble, or E4M3, one byte each.  A
+ * row-major [rows, cols] matrix has codes [rows, cols / 2] or [rows, cols] and scales
+ * [rows, cols / 32].
+ *
+ * quantize_mx.  src bf16 or fp32 [rows, cols] -> codes, scales.  With m a block's largest
+ * magnitude the scale is 2^(floor(log2 m) - e), clamped to 2^-127 .. 2^127, e = 2
+ * for E2M1 and 8 for E4M3; elements are value / scale rounded to the nearest format
+ * value, ties to even, saturating at 6 and 448 (so the top of a block may lose up
+ * to a quarter, E4M3 an eighth).  A block that holds an infinity or a NaN gets scale
+ * code 255 (and E4M3 codes 0x7F, E2M1 codes 0).
+ *   cols < 32 or not a multiple of 32, rows < 1, rows*cols > 2^40 -> MOE_ERR_UNSUPPORTED_SHAPE
+ *   an unknown src_type or format                                 -> MOE_ERR_INVALID_ARG */
+#define MOE_SRC_BF16 0
+#define MOE_SRC_F32 1
+#define MOE_MX_E2M1 0
+#define MOE_MX_E4M3 1
+moe_status_t moe_quantize_mx(const void* src, int src_type, int64_t rows, int64_t cols, int format,
+                             uint8_t* codes, uint8_t* scales, moe_stream_t stream);
+
+/* add_rmsnorm.  h = bf16(x + residual); n = h * weight / sqrt(mean(h^2) + eps) over the
+ * H columns, in fp32 -> sum = h, out = bf16(n), codes / scales = n in MX E4M3
+ * blocks (quantised from the fp32 n, not from out).  x, residual, sum and out bf16
+ * [T, H], weight bf16 [H].  Without a residual (NULL, then sum is NULL too) h = x.
+ * out may be NULL, or codes and scales may (both), not all three.  sum may be the
+ * residual's own buffer; nothing else may alias.
+ *   T < 1, H < 32, H > 65536 or H not a multiple of 32 -> MOE_ERR_UNSUPPORTED_SHAPE
+ *   eps negative or NaN                                -> MOE_ERR_INVALID_ARG */
+moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const moe_bf16_t* residual,
+                             const moe_bf16_t* weight, int32_t T, int32_t H, float eps,
+                             moe_bf16_t* sum, moe_bf16_t* out, uint8_t* codes, uint8_t* scales,
+                             moe_stream_t stream);
+
+/* grouped_mm_mx4.  R token rows in expert order: y[r] = w[e] . a[r] for expert_offsets[e]
+ * <= r < expert_offsets[e + 1], summed in fp32 and rounded once to bf16.  a MX E4M3
+ * [R, K], w MX E2M1 [E, N, K], expert_offsets int32 [E + 1], ascending from 0 to at
+ * most R -> y bf16 [R, N]; rows from expert_offsets[E] on are left as they were.
+ *   R < 1, R > 2^30, E < 1, E > 1024, N < 8 or not a multiple of 8, K < 128 or not a
+ *   multiple of 128, or a size overflow                 -> MOE_ERR_UNSUPPORTED_SHAPE
+ *   w not 32-byte aligned (others: 16)                  -> MOE_ERR_MISALIGNED
+ * The workspace (moe_grouped_mm_workspace_size bytes) holds the error word that
+ * moe_device_status reads. */
+typedef struct {
+    int32_t R, E, N, K;
+} moe_mm_shape_t;
+size_t moe_grouped_mm_workspace_size(moe_mm_shape_t shape);
+moe_status_t moe_grouped_mm_mx4(const uint8_t* a, const uint8_t* a_scale, const uint8_t* w,
+                                const uint8_t* w_scale, const int32_t* expert_offsets,
+                                moe_mm_shape_t shape, moe_bf16_t* y, void* workspace,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace bytes of moe_grouped_ffn_mx4 and moe_forward_mx4 (0: unsupported shape). */
+size_t moe_mx4_workspace_size(moe_shape_t shape);
+
+/* grouped_ffn_mx4.  moe_grouped_ffn on microscaled operands: x MX E4M3 [T, H]; w13 MX
+ * E2M1 [E, 2I, H]; w2 MX E2M1 [E, H, I] -> y bf16 [T*k, H] in expanded-id order.  Both
+ * products are summed in fp32; act = silu(gate) * up becomes MX E4M3 [T*k, I], rounded
+ * from fp32.  Any T; the shape rules are moe_grouped_ffn's, w13 and w2 32-byte
+ * aligned, the workspace of moe_mx4_workspace_size.  expert_offsets[E] is T*k. */
+moe_status_t moe_grouped_ffn_mx4(const uint8_t* x, const uint8_t* x_scale, const uint8_t* w13,
+                                 const uint8_t* w13_scale, const uint8_t* w2,
+                                 const uint8_t* w2_scale, const int32_t* expert_offsets,
+                                 const int32_t* permuted_rows, moe_shape_t shape, moe_bf16_t* y,
+                                 void* workspace, size_t ws_bytes, moe_stream_t stream);
+
+/* The whole layer on microscaled operands, any T: route -> permute ->
+ * grouped_ffn_mx4 -> combine.  Other arguments and outputs as moe_forward; the
+ * workspace is that of moe_mx4_workspace_size. */
+moe_status_t moe_forward_mx4(const uint8_t* x, const uint8_t* x_scale, const float* logits,
+                             const uint8_t* w13, const uint8_t* w13_scale, const uint8_t* w2,
+                             const uint8_t* w2_scale, moe_shape_t shape, moe_bf16_t* out,
+                             int32_t* topk_ids, float* topk_weights, int32_t* expert_offsets,
+                             int32_t* permuted_rows, void* workspace, size_t ws_bytes,
+                             moe_stream_t stream);
+
 /* Number of kernels one moe_forward call launches for `shape` (0 if unsupported). */
 int moe_forward_kernel_count(moe_shape_t shape);
 

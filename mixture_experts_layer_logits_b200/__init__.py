@@ -23,6 +23,9 @@ __all__ = [
     "MOE_OK", "MOE_ERR_INVALID_ARG", "MOE_ERR_UNSUPPORTED_SHAPE", "MOE_ERR_MISALIGNED",
     "MOE_ERR_WORKSPACE_TOO_SMALL", "MOE_ERR_CUDA", "MOE_ERR_DEVICE_TIMEOUT",
     "MOE_ERR_DEVICE_BOUNDS", "debug_library_path",
+    "MmShape", "moe_quantize_mx", "moe_add_rmsnorm", "moe_grouped_mm_workspace_size",
+    "moe_grouped_mm_mx4", "moe_mx4_workspace_size", "moe_grouped_ffn_mx4", "moe_forward_mx4",
+    "workspace_mx4",
 ]
 
 (MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED_SHAPE, MOE_ERR_MISALIGNED,
@@ -46,6 +49,13 @@ class Shape(ctypes.Structure):
 
     def __repr__(self):
         return f"Shape(T={self.T}, E={self.E}, top_k={self.top_k}, H={self.H}, I={self.I})"
+
+
+class MmShape(ctypes.Structure):
+    """moe_mm_shape_t: R token rows, E experts, N outputs, K inputs."""
+
+    _fields_ = [("R", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
+                ("K", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -95,6 +105,20 @@ def load_library():
                                               ctypes.c_void_p]
     lib.moe_selftest_wait_timeout.restype = ctypes.c_int
     lib.moe_device_status.argtypes = [_vp, ctypes.c_size_t, _vp]
+    i64, sz = ctypes.c_int64, ctypes.c_size_t
+    lib.moe_quantize_mx.argtypes = [_vp, ctypes.c_int, i64, i64, ctypes.c_int, _vp, _vp, _vp]
+    lib.moe_add_rmsnorm.argtypes = [_vp, _vp, _vp, ctypes.c_int32, ctypes.c_int32, ctypes.c_float,
+                                    _vp, _vp, _vp, _vp, _vp]
+    lib.moe_grouped_mm_workspace_size.argtypes = [MmShape]
+    lib.moe_grouped_mm_workspace_size.restype = sz
+    lib.moe_grouped_mm_mx4.argtypes = [_vp] * 5 + [MmShape, _vp, _vp, sz, _vp]
+    lib.moe_mx4_workspace_size.argtypes = [Shape]
+    lib.moe_mx4_workspace_size.restype = sz
+    lib.moe_grouped_ffn_mx4.argtypes = [_vp] * 8 + [Shape, _vp, _vp, sz, _vp]
+    lib.moe_forward_mx4.argtypes = [_vp] * 7 + [Shape] + [_vp] * 6 + [sz, _vp]
+    for fn in (lib.moe_quantize_mx, lib.moe_add_rmsnorm, lib.moe_grouped_mm_mx4,
+               lib.moe_grouped_ffn_mx4, lib.moe_forward_mx4):
+        fn.restype = ctypes.c_int
     for fn in (lib.moe_route, lib.moe_permute, lib.moe_grouped_ffn, lib.moe_combine,
                lib.moe_forward, lib.moe_forward_timed, lib.moe_forward_w8,
                lib.moe_forward_w8_timed, lib.moe_device_status):
@@ -285,6 +309,211 @@ def moe_forward_kernel_count(T: int, E: int, top_k: int, H: int, I: int) -> int:
 def moe_forward_fused(T: int, E: int, top_k: int, H: int, I: int) -> bool:
     """True if moe_forward runs the FFN and the combine as one persistent launch."""
     return bool(load_library().moe_forward_fused(Shape(T, E, top_k, H, I)))
+
+
+# ------------------------------------------------------------------ microscaled operators
+#
+# These calls run on the current stream of their tensors' device, whichever device is
+# current, and check that all tensors are on that one.
+
+_MX_FORMATS = {"e2m1": 0, "e4m3": 1}
+_MX_SOURCES = {torch.bfloat16: 0, torch.float32: 1}
+
+
+def _same(t: torch.Tensor, name: str, dtype, shape, device):
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _out(t, name, dtype, shape, device):
+    """The given output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _same(t, name, dtype, torch.Size(shape), device)
+    return t
+
+
+def _call(fn, where, device, *args):
+    """fn(*args, current stream of `device`) with that device current."""
+    if device.type != "cuda":
+        raise ValueError(f"{where}: expected CUDA tensors, got {device}")
+    index = device.index
+    stream = torch.cuda.current_stream(index).cuda_stream
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != MOE_OK:
+        raise MoeError(status, where)
+
+
+def moe_quantize_mx(src: torch.Tensor, fmt: str = "e2m1", codes=None, scales=None):
+    """(codes, scales): src (bf16 or fp32 [..., cols], cols a multiple of 32) in microscaled
+    blocks of 32 columns.  fmt "e2m1": codes uint8 [..., cols / 2], the lower column in
+    the low nibble; "e4m3": codes uint8 [..., cols].  scales uint8 [..., cols / 32],
+    2^(code - 127)."""
+    if fmt not in _MX_FORMATS:
+        raise ValueError(f"fmt: expected 'e2m1' or 'e4m3', got {fmt!r}")
+    if src.dtype not in _MX_SOURCES or src.dim() < 1 or not src.is_contiguous():
+        raise ValueError(f"src: expected a contiguous bf16 or fp32 matrix, got {src.dtype} "
+                         f"{tuple(src.shape)}")
+    *lead, cols = src.shape
+    if cols < 32 or cols % 32 or src.numel() == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_quantize_mx")
+    dev = src.device
+    codes = _out(codes, "codes", torch.uint8, (*lead, cols // 2 if fmt == "e2m1" else cols), dev)
+    scales = _out(scales, "scales", torch.uint8, (*lead, cols // 32), dev)
+    _call(load_library().moe_quantize_mx, "moe_quantize_mx", dev, src.data_ptr(),
+          _MX_SOURCES[src.dtype], src.numel() // cols, cols, _MX_FORMATS[fmt], codes.data_ptr(),
+          scales.data_ptr())
+    return codes, scales
+
+
+def moe_add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool = False,
+                    sum_out=None, out=None, codes=None, scales=None):
+    """(h, out, codes, scales): h = bf16(x + residual) and its root-mean-square norm times
+    weight, as bf16 `out` and, with quantize=True, in microscaled E4M3 blocks (codes uint8
+    [T, H], scales uint8 [T, H / 32]); codes and scales are None without it.  x, residual bf16
+    [T, H], weight bf16 [H].  Without a residual h is None and x itself is normed.
+    sum_out may be the residual, which is then updated in place."""
+    if x.dim() != 2:
+        raise ValueError(f"x: expected [T, H], got {tuple(x.shape)}")
+    shape, dev = x.shape, x.device
+    T, H = shape
+    if T < 1 or H < 32 or H % 32:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_add_rmsnorm")
+    bf16 = torch.bfloat16
+    px = _same(x, "x", bf16, shape, dev)
+    pw = _same(weight, "weight", bf16, torch.Size((H,)), dev)
+    pr = ps = pc = psc = None
+    if residual is not None:
+        pr = _same(residual, "residual", bf16, shape, dev)
+        sum_out = _out(sum_out, "sum_out", bf16, shape, dev)
+        ps = sum_out.data_ptr()
+    elif sum_out is not None:
+        raise ValueError("sum_out: there is no residual to add")
+    out = _out(out, "out", bf16, shape, dev)
+    if quantize:
+        codes = _out(codes, "codes", torch.uint8, shape, dev)
+        scales = _out(scales, "scales", torch.uint8, (T, H // 32), dev)
+        pc, psc = codes.data_ptr(), scales.data_ptr()
+    elif codes is not None or scales is not None:
+        raise ValueError("codes, scales: given without quantize=True")
+    _call(load_library().moe_add_rmsnorm, "moe_add_rmsnorm", dev, px, pr, pw, T, H, eps, ps,
+          out.data_ptr(), pc, psc)
+    return sum_out, out, codes, scales
+
+
+def moe_grouped_mm_workspace_size(R: int, E: int, N: int, K: int) -> int:
+    return int(load_library().moe_grouped_mm_workspace_size(MmShape(R, E, N, K)))
+
+
+def moe_grouped_mm_mx4(a, a_scale, w, w_scale, expert_offsets, ws=None, y=None):
+    """y bf16 [R, N]: rows expert_offsets[e] .. expert_offsets[e + 1] of a (microscaled E4M3
+    codes uint8 [R, K], scales uint8 [R, K / 32]) times w[e] transposed (E2M1 codes uint8
+    [E, N, K / 2], scales uint8 [E, N, K / 32]).  Rows behind expert_offsets[E] are not
+    written."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError(f"a, w: expected [R, K] and [E, N, K / 2], got {tuple(a.shape)} and "
+                         f"{tuple(w.shape)}")
+    R, K = a.shape
+    E, N, _ = w.shape
+    dev, u8, size = a.device, torch.uint8, torch.Size
+    need = moe_grouped_mm_workspace_size(R, E, N, K)
+    if need == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_grouped_mm_mx4")
+    ptrs = (_same(a, "a", u8, size((R, K)), dev),
+            _same(a_scale, "a_scale", u8, size((R, K // 32)), dev),
+            _same(w, "w", u8, size((E, N, K // 2)), dev),
+            _same(w_scale, "w_scale", u8, size((E, N, K // 32)), dev),
+            _same(expert_offsets, "expert_offsets", torch.int32, size((E + 1,)), dev))
+    y = _out(y, "y", torch.bfloat16, (R, N), dev)
+    ws = _workspace_of(ws, need, dev)
+    _call(load_library().moe_grouped_mm_mx4, "moe_grouped_mm_mx4", dev, *ptrs,
+          MmShape(R, E, N, K), y.data_ptr(), ws.data_ptr(), ws.numel())
+    return y
+
+
+def moe_mx4_workspace_size(T: int, E: int, top_k: int, H: int, I: int) -> int:
+    return int(load_library().moe_mx4_workspace_size(Shape(T, E, top_k, H, I)))
+
+
+def workspace_mx4(T: int, E: int, top_k: int, H: int, I: int, device="cuda") -> torch.Tensor:
+    """A device workspace of moe_grouped_ffn_mx4 and moe_forward_mx4 for the shape (uint8)."""
+    n = moe_mx4_workspace_size(T, E, top_k, H, I)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_mx4_workspace_size")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _workspace_of(ws, need, device):
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous uint8 on {device}, got {ws.dtype} on {ws.device}")
+    return ws
+
+
+def _mx4_operands(where, x, x_scale, w13, w13_scale, w2, w2_scale, top_k):
+    """(Shape, workspace bytes, pointers) of the checked x and weights."""
+    if x.dim() != 2 or w13.dim() != 3 or w2.dim() != 3:
+        raise ValueError(f"{where}: expected x [T, H], w13 [E, 2I, H / 2] and w2 [E, H, I / 2]")
+    T, H = x.shape
+    E = w13.shape[0]
+    I = w13.shape[1] // 2
+    shape = Shape(T, E, top_k, H, I)
+    need = int(load_library().moe_mx4_workspace_size(shape))
+    if need == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, where)
+    dev, u8, size = x.device, torch.uint8, torch.Size
+    return shape, need, (
+        _same(x, "x", u8, size((T, H)), dev),
+        _same(x_scale, "x_scale", u8, size((T, H // 32)), dev),
+        _same(w13, "w13", u8, size((E, 2 * I, H // 2)), dev),
+        _same(w13_scale, "w13_scale", u8, size((E, 2 * I, H // 32)), dev),
+        _same(w2, "w2", u8, size((E, H, I // 2)), dev),
+        _same(w2_scale, "w2_scale", u8, size((E, H, I // 32)), dev))
+
+
+def moe_grouped_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, expert_offsets, permuted_rows,
+                        top_k: int, ws=None, y=None):
+    """moe_grouped_ffn on microscaled operands: x E4M3 codes uint8 [T, H], w13 and w2 E2M1
+    codes uint8 [E, 2I, H / 2] and [E, H, I / 2], each with its uint8 scales
+    [..., cols / 32]; y bf16 [T*k, H].  act is microscaled E4M3 between the two products."""
+    shape, need, ptrs = _mx4_operands("moe_grouped_ffn_mx4", x, x_scale, w13, w13_scale, w2,
+                                      w2_scale, top_k)
+    dev, R = x.device, shape.T * top_k
+    off = _same(expert_offsets, "expert_offsets", torch.int32, torch.Size((shape.E + 1,)), dev)
+    rows = _same(permuted_rows, "permuted_rows", torch.int32, torch.Size((R,)), dev)
+    y = _out(y, "y", torch.bfloat16, (R, shape.H), dev)
+    ws = _workspace_of(ws, need, dev)
+    _call(load_library().moe_grouped_ffn_mx4, "moe_grouped_ffn_mx4", dev, *ptrs, off, rows, shape,
+          y.data_ptr(), ws.data_ptr(), ws.numel())
+    return y
+
+
+def moe_forward_mx4(x, x_scale, logits, w13, w13_scale, w2, w2_scale, top_k: int, ws=None,
+                    out=None, topk_ids=None, topk_weights=None, expert_offsets=None,
+                    permuted_rows=None):
+    """The whole layer on microscaled operands (see moe_grouped_ffn_mx4), any T.  Other
+    arguments and outputs as moe_forward; ws of workspace_mx4."""
+    shape, need, ptrs = _mx4_operands("moe_forward_mx4", x, x_scale, w13, w13_scale, w2, w2_scale,
+                                      top_k)
+    dev, T, E = x.device, shape.T, shape.E
+    plog = _same(logits, "logits", torch.float32, torch.Size((T, E)), dev)
+    extra = [None if t is None else _same(t, name, dt, torch.Size(shp), dev)
+             for t, name, dt, shp in ((topk_ids, "topk_ids", torch.int32, (T, top_k)),
+                                      (topk_weights, "topk_weights", torch.float32, (T, top_k)),
+                                      (expert_offsets, "expert_offsets", torch.int32, (E + 1,)),
+                                      (permuted_rows, "permuted_rows", torch.int32, (T * top_k,)))]
+    out = _out(out, "out", torch.bfloat16, (T, shape.H), dev)
+    ws = _workspace_of(ws, need, dev)
+    _call(load_library().moe_forward_mx4, "moe_forward_mx4", dev, *ptrs[:2], plog, *ptrs[2:],
+          shape, out.data_ptr(), *extra, ws.data_ptr(), ws.numel())
+    return out
 
 
 def moe_selftest_wait_timeout(ws: torch.Tensor, limit_us: int) -> None:

@@ -227,4 +227,44 @@ cudaError_t launch_swiglu_finalize(const float* partials, const int32_t* splits,
 cudaError_t launch_reduce_y(const float* partials, const int32_t* splits, int R, int H, void* y,
                             cudaStream_t st);
 
+// ------------------------------------------------------------------ microscaled operators
+
+// h = bf16(x + residual) (x itself without a residual), n = h * weight / sqrt(mean(h^2) +
+// eps) as bf16 in `out` and as E4M3 blocks in codes / scales; each of the two may be null.
+struct NormArgs {
+    const void* x;         // bf16 [T, H]
+    const void* residual;  // bf16 [T, H] or null
+    const void* weight;    // bf16 [H]
+    void* sum;             // bf16 [T, H], null without a residual; may be `residual` itself
+    void* out;             // bf16 [T, H]
+    uint8_t* codes;        // [T, H]
+    uint8_t* scales;       // [T, H / 32]
+    int T, H;
+    float eps;
+};
+constexpr int kMaxNormH = 65536;
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st);
+
+// MX blocks of n consecutive elements (bf16, or fp32 with f32).
+cudaError_t launch_quantize_mx(const void* src, bool f32, long n, bool e2m1, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t st);
+
+// One product grouped by expert.  Mode 0: act = MX(silu(gate) * up) of rows a[rows[p] / k]
+// (N = I act features, w has 2N rows an expert); mode 1: y[rows[p]] = w a[p]; mode 2:
+// y[p] = w a[p].
+struct MxArgs {
+    const uint8_t* a;        // E4M3 codes [.., K]
+    const uint8_t* a_scale;  // [.., K / 32]
+    const uint8_t* w;        // E2M1 codes [E, N or 2N, K / 2]
+    const uint8_t* w_scale;  // [E, N or 2N, K / 32]
+    const int32_t* offsets;  // [E + 1]
+    const int32_t* rows;     // [R] (modes 0 and 1)
+    uint8_t* act;            // mode 0: [R, N] and [R, N / 32]
+    uint8_t* act_scale;
+    void* y;                 // modes 1 and 2: bf16 [R, N]
+    int32_t* err;
+    int E, R, k, N, K;
+};
+cudaError_t launch_mx_grouped(const MxArgs& g, int mode, cudaStream_t st);
+
 }  // namespace moe

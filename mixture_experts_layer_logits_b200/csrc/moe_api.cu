@@ -237,6 +237,76 @@ moe_status_t run_ffn(const void* x, const void* w13, const void* w2, const int32
         mid_event ? static_cast<cudaEvent_t>(mid_event[0]) : nullptr, reduce_y));
 }
 
+// Operands of a microscaled product are read by TMA, whose 4-bit loads want 32-byte
+// aligned tensors.
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
+bool mm_shape_ok(const moe_mm_shape_t& s)
+{
+    if (s.R < 1 || s.R > (1 << 30) || s.E < 1 || s.E > 1024) return false;
+    if (s.N < 8 || s.N % 8 || s.K < 128 || s.K % 128) return false;
+    if ((long long)s.E * s.N > INT_MAX) return false;  // TMA row coordinates
+    return (long long)s.R * s.N <= (1LL << 40) && (long long)s.R * s.K <= (1LL << 40);
+}
+
+// The routing part of layout_for, then what the microscaled FFN keeps.
+struct MxLayout {
+    Layout route;
+    size_t act, act_scale, y, total;
+};
+
+MxLayout mx_layout_for(const moe_shape_t& s)
+{
+    moe_shape_t rs = s;
+    rs.H = rs.I = 0;
+    MxLayout L;
+    L.route = layout_for(rs);
+    const size_t R = (size_t)s.T * s.top_k;
+    size_t off = L.route.total;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = align_up(off + bytes);
+        return at;
+    };
+    L.act = take(R * s.I);
+    L.act_scale = take(R * (s.I / 32));
+    L.y = take(R * s.H * 2);
+    L.total = off;
+    return L;
+}
+
+moe_status_t run_ffn_mx4(const uint8_t* x, const uint8_t* x_scale, const uint8_t* w13,
+                         const uint8_t* w13_scale, const uint8_t* w2, const uint8_t* w2_scale,
+                         const int32_t* offsets, const int32_t* rows, const moe_shape_t& s,
+                         void* y, void* ws, const MxLayout& L, cudaStream_t st)
+{
+    MxArgs g = {};
+    g.a = x;
+    g.a_scale = x_scale;
+    g.w = w13;
+    g.w_scale = w13_scale;
+    g.offsets = offsets;
+    g.rows = rows;
+    g.act = at<uint8_t>(ws, L.act);
+    g.act_scale = at<uint8_t>(ws, L.act_scale);
+    g.err = at<int32_t>(ws, L.route.err);
+    g.E = s.E;
+    g.R = s.T * s.top_k;
+    g.k = s.top_k;
+    g.N = s.I;
+    g.K = s.H;
+    cudaError_t e = launch_mx_grouped(g, 0, st);
+    if (e != cudaSuccess) return cuda_status(e);
+    g.a = g.act;
+    g.a_scale = g.act_scale;
+    g.w = w2;
+    g.w_scale = w2_scale;
+    g.y = y;
+    g.N = s.H;
+    g.K = s.I;
+    return cuda_status(launch_mx_grouped(g, 1, st));
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -463,6 +533,124 @@ int moe_forward_fused(moe_shape_t s)
 {
     if (!ffn_shape_ok(s)) return 0;
     return layout_for(s).fused && fused_enabled() ? 1 : 0;
+}
+
+moe_status_t moe_quantize_mx(const void* src, int src_type, int64_t rows, int64_t cols, int format,
+                             uint8_t* codes, uint8_t* scales, moe_stream_t stream)
+{
+    if (!src || !codes || !scales) return MOE_ERR_INVALID_ARG;
+    if ((src_type != MOE_SRC_BF16 && src_type != MOE_SRC_F32) ||
+        (format != MOE_MX_E2M1 && format != MOE_MX_E4M3))
+        return MOE_ERR_INVALID_ARG;
+    if (rows < 1 || cols < 32 || cols % 32 || rows > (1LL << 40) / cols)
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(src) || !aligned16(codes) || !aligned16(scales)) return MOE_ERR_MISALIGNED;
+    return cuda_status(launch_quantize_mx(src, src_type == MOE_SRC_F32, (long)(rows * cols),
+                                          format == MOE_MX_E2M1, codes, scales,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const moe_bf16_t* residual,
+                             const moe_bf16_t* weight, int32_t T, int32_t H, float eps,
+                             moe_bf16_t* sum, moe_bf16_t* out, uint8_t* codes, uint8_t* scales,
+                             moe_stream_t stream)
+{
+    if (!x || !weight || (!out && !codes) || !residual != !sum || !codes != !scales)
+        return MOE_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (T < 1 || H < 32 || H % 32 || H > kMaxNormH) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(sum) ||
+        !aligned16(out) || !aligned16(codes) || !aligned16(scales))
+        return MOE_ERR_MISALIGNED;
+    NormArgs a = {x, residual, weight, sum, out, codes, scales, T, H, eps};
+    return cuda_status(launch_add_rmsnorm(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_grouped_mm_workspace_size(moe_mm_shape_t s)
+{
+    return mm_shape_ok(s) ? kAlign : 0;
+}
+
+moe_status_t moe_grouped_mm_mx4(const uint8_t* a, const uint8_t* a_scale, const uint8_t* w,
+                                const uint8_t* w_scale, const int32_t* expert_offsets,
+                                moe_mm_shape_t s, moe_bf16_t* y, void* ws, size_t ws_bytes,
+                                moe_stream_t stream)
+{
+    if (!a || !a_scale || !w || !w_scale || !expert_offsets || !y || !ws)
+        return MOE_ERR_INVALID_ARG;
+    if (!mm_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(a) || !aligned16(a_scale) || !aligned32(w) || !aligned16(w_scale) ||
+        !aligned16(expert_offsets) || !aligned16(y) || !aligned16(ws))
+        return MOE_ERR_MISALIGNED;
+    if (ws_bytes < moe_grouped_mm_workspace_size(s)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    MxArgs g = {};
+    g.a = a;
+    g.a_scale = a_scale;
+    g.w = w;
+    g.w_scale = w_scale;
+    g.offsets = expert_offsets;
+    g.y = y;
+    g.err = static_cast<int32_t*>(ws);
+    g.E = s.E;
+    g.R = s.R;
+    g.N = s.N;
+    g.K = s.K;
+    return cuda_status(launch_mx_grouped(g, 2, static_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_mx4_workspace_size(moe_shape_t s)
+{
+    return ffn_shape_ok(s) ? mx_layout_for(s).total : 0;
+}
+
+moe_status_t moe_grouped_ffn_mx4(const uint8_t* x, const uint8_t* x_scale, const uint8_t* w13,
+                                 const uint8_t* w13_scale, const uint8_t* w2,
+                                 const uint8_t* w2_scale, const int32_t* expert_offsets,
+                                 const int32_t* permuted_rows, moe_shape_t s, moe_bf16_t* y,
+                                 void* ws, size_t ws_bytes, moe_stream_t stream)
+{
+    if (!x || !x_scale || !w13 || !w13_scale || !w2 || !w2_scale || !expert_offsets ||
+        !permuted_rows || !y || !ws)
+        return MOE_ERR_INVALID_ARG;
+    if (!ffn_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(x_scale) || !aligned32(w13) || !aligned16(w13_scale) ||
+        !aligned32(w2) || !aligned16(w2_scale) || !aligned16(expert_offsets) ||
+        !aligned16(permuted_rows) || !aligned16(y) || !aligned16(ws))
+        return MOE_ERR_MISALIGNED;
+    const MxLayout L = mx_layout_for(s);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    return run_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, expert_offsets, permuted_rows, s,
+                       y, ws, L, static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_forward_mx4(const uint8_t* x, const uint8_t* x_scale, const float* logits,
+                             const uint8_t* w13, const uint8_t* w13_scale, const uint8_t* w2,
+                             const uint8_t* w2_scale, moe_shape_t s, moe_bf16_t* out,
+                             int32_t* topk_ids, float* topk_weights, int32_t* expert_offsets,
+                             int32_t* permuted_rows, void* ws, size_t ws_bytes,
+                             moe_stream_t stream)
+{
+    if (!x || !x_scale || !logits || !w13 || !w13_scale || !w2 || !w2_scale || !out || !ws)
+        return MOE_ERR_INVALID_ARG;
+    if (!ffn_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(x) || !aligned16(x_scale) || !aligned16(logits) || !aligned32(w13) ||
+        !aligned16(w13_scale) || !aligned32(w2) || !aligned16(w2_scale) || !aligned16(out) ||
+        !aligned16(ws) || !aligned16(topk_ids) || !aligned16(topk_weights) ||
+        !aligned16(expert_offsets) || !aligned16(permuted_rows))
+        return MOE_ERR_MISALIGNED;
+    const MxLayout L = mx_layout_for(s);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    int32_t* ids = topk_ids ? topk_ids : at<int32_t>(ws, L.route.ids);
+    float* wts = topk_weights ? topk_weights : at<float>(ws, L.route.weights);
+    int32_t* offs = expert_offsets ? expert_offsets : at<int32_t>(ws, L.route.offsets);
+    int32_t* rows = permuted_rows ? permuted_rows : at<int32_t>(ws, L.route.rows);
+    void* y = at<void>(ws, L.y);
+    moe_status_t r = run_permute(logits, ids, wts, s, offs, rows, ws, L.route, st);
+    if (r == MOE_OK)
+        r = run_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, offs, rows, s, y, ws, L, st);
+    if (r == MOE_OK) r = cuda_status(launch_combine(y, wts, s.T, s.top_k, s.H, out, st));
+    return r;
 }
 
 moe_status_t moe_device_status(void* ws, size_t ws_bytes, moe_stream_t stream)

@@ -1,0 +1,177 @@
+// mx_quant.cu -- the HBM-bound producers of microscaled rows: quantisation of a
+// matrix, and the residual addition with root-mean-square norm.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kernels.h"
+#include "mx_common.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+__device__ __forceinline__ void unpack_bf16x8(const uint4& q, float (&v)[8])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------ quantisation
+
+// A matrix whose columns are a multiple of 32 is a run of blocks, whatever its rows:
+// four consecutive threads hold one block, 8 elements each.
+template <bool E2M1, typename Src>
+__global__ void __launch_bounds__(256)
+    quantize_kernel(const Src* __restrict__ src, long chunks, uint8_t* __restrict__ codes,
+                    uint8_t* __restrict__ scales)
+{
+    pdl_launch_dependents();
+    pdl_wait();
+    const long c = (long)blockIdx.x * blockDim.x + threadIdx.x;  // 8-element chunk
+    const bool live = c < chunks;
+    float v[8] = {};
+    if (live) {
+        if constexpr (sizeof(Src) == 2) {
+            unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(src) + c), v);
+        } else {
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(src) + 2 * c);
+            const float4 b = __ldcs(reinterpret_cast<const float4*>(src) + 2 * c + 1);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        }
+    }
+    uint2 q;
+    const uint32_t s = mx::quantize8<E2M1>(v, q);
+    if (!live) return;
+    if constexpr (E2M1)
+        reinterpret_cast<uint32_t*>(codes)[c] = q.x;
+    else
+        reinterpret_cast<uint2*>(codes)[c] = q;
+    if ((c & 3) == 0) scales[c >> 2] = (uint8_t)s;
+}
+
+// ------------------------------------------------------------------ norm
+
+// One row per CTA.  h = x + residual rounded to bf16 (that is what the next layer
+// reads, so the norm is the norm of the stored sum), r = 1 / sqrt(mean(h^2) + eps),
+// n = (h * weight) * r: the product of two bf16 values is exact in fp32, so n carries
+// the rounding of r and of one product.  Sums are fp32.
+template <int C>
+__global__ void __launch_bounds__(1024)
+    rmsnorm_kernel(const uint4* __restrict__ x, const uint4* residual,
+                   const uint4* __restrict__ weight, int chunks, float inv_h, float eps,
+                   uint4* sum, uint4* __restrict__ out, uint8_t* __restrict__ codes,
+                   uint8_t* __restrict__ scales)
+{
+    __shared__ float part[32];
+    pdl_launch_dependents();
+    pdl_wait();
+    const size_t base = (size_t)blockIdx.x * chunks;
+    uint4 h[C];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        if (c >= chunks) continue;
+        h[i] = x[base + c];
+        float v[8];
+        unpack_bf16x8(h[i], v);
+        if (residual) {
+            float r[8];
+            unpack_bf16x8(residual[base + c], r);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += r[j];
+            h[i] = pack_bf16x8(v);
+            sum[base + c] = h[i];
+            unpack_bf16x8(h[i], v);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
+    __syncthreads();
+    ss = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float r = 1.0f / sqrtf(fmaf(ss, inv_h, eps));
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int c = threadIdx.x + i * blockDim.x;
+        const bool live = c < chunks;
+        float v[8] = {};
+        if (live) {
+            float w[8];
+            unpack_bf16x8(h[i], v);
+            unpack_bf16x8(weight[c], w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (v[j] * w[j]) * r;
+            if (out) out[base + c] = pack_bf16x8(v);
+        }
+        if (codes) {
+            uint2 q;
+            const uint32_t s = mx::quantize8<false>(v, q);
+            if (live) {
+                reinterpret_cast<uint2*>(codes)[base + c] = q;
+                if ((c & 3) == 0) scales[(base + c) >> 2] = (uint8_t)s;
+            }
+        }
+    }
+}
+
+template <int C>
+cudaError_t launch_norm(const NormArgs& a, int threads, cudaStream_t st)
+{
+    return launch_pdl(rmsnorm_kernel<C>, dim3(a.T), dim3(threads), 0, st,
+                      static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.residual),
+                      static_cast<const uint4*>(a.weight), a.H / 8, 1.0f / (float)a.H, a.eps,
+                      static_cast<uint4*>(a.sum), static_cast<uint4*>(a.out), a.codes, a.scales);
+}
+
+}  // namespace
+
+cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st)
+{
+    const int chunks = a.H / 8;
+    const int c = (chunks + 1023) / 1024;  // 8-element chunks per thread
+    const int threads = ((chunks + c - 1) / c + 31) & ~31;
+    if (c <= 1) return launch_norm<1>(a, threads, st);
+    if (c <= 2) return launch_norm<2>(a, threads, st);
+    if (c <= 4) return launch_norm<4>(a, threads, st);
+    return launch_norm<8>(a, threads, st);
+}
+
+cudaError_t launch_quantize_mx(const void* src, bool f32, long n, bool e2m1, uint8_t* codes,
+                               uint8_t* scales, cudaStream_t st)
+{
+    const long chunks = n / 8;
+    const dim3 grid((unsigned)((chunks + 255) / 256)), block(256);
+    if (f32) {
+        const float* s = static_cast<const float*>(src);
+        return e2m1 ? launch_pdl(quantize_kernel<true, float>, grid, block, 0, st, s, chunks, codes, scales)
+                    : launch_pdl(quantize_kernel<false, float>, grid, block, 0, st, s, chunks, codes, scales);
+    }
+    const uint16_t* s = static_cast<const uint16_t*>(src);
+    return e2m1 ? launch_pdl(quantize_kernel<true, uint16_t>, grid, block, 0, st, s, chunks, codes, scales)
+                : launch_pdl(quantize_kernel<false, uint16_t>, grid, block, 0, st, s, chunks, codes, scales);
+}
+
+}  // namespace moe
