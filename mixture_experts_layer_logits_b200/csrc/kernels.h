@@ -264,6 +264,10 @@ struct MxArgs {
     void* y;                 // modes 1 and 2: bf16 [R, N]
     int32_t* err;
     int E, R, k, N, K;
+    // set by launch_mx_grouped
+    int fb_count;            // feature blocks of an expert
+    int early;               // only `a` comes from the launch before
+    int stream_weights;      // weights are read once: evict first
 };
 cudaError_t launch_mx_grouped(const MxArgs& g, int mode, cudaStream_t st);
 

@@ -1,11 +1,38 @@
-// mx_ffn.cu -- products grouped by expert of E4M3 rows with E2M1 weights (both in
-// microscaled blocks), alone and as the two products of the expert FFN.
+// mx_ffn.cu -- products grouped by expert of E4M3 token rows with E2M1 weights (both in
+// microscaled blocks of 32 with E8M0 scales), alone and as the two products of the
+// expert FFN, on block-scaled tcgen05 tensor cores:
+//   D[f, j] = sum_b 2^(sw[f, b] + sa[j, b] - 254) sum_{i in block b} w[f, i] a[j, i]
+// in fp32.  Products of codes and their power-of-two scales are exact, so only the
+// fp32 sums round.
+//
+// Two launches of one persistent, warp-specialised kernel make the FFN:
+//   MODE 0  act[p, f] = MX(silu(gate) * up) of x[rows[p] / k] with w13[e] rows f and I + f
+//   MODE 1  y[rows[p] or p, f] = w[e] row f dotted with act (or any E4M3 rows) [p]
+//
+// The MMA's M = 128 rows are weight rows and its N columns the token rows of one
+// expert, rounded up to 16 per tile: few tokens cost few columns, and a ragged group
+// costs at most 15 padded ones.  MODE 0's 128 weight rows are 64 gate rows and their
+// 64 up rows.
+//
+// Warp roles: 0 TMA (weights, MODE 1 also token rows); 1 TMEM and MMA issue; 2-3
+// scales; 4-11 epilogue; MODE 0: 12-15 gather of token rows.
+//   - Weights: TMA unpacks the 4-bit codes to the byte-wide slots that a mixed
+//     E2M1 x E4M3 MMA reads, so HBM and L2 move half a byte an element.
+//   - Scales: a K tile of 128 has 4 scale bytes per row.  They are copied 4 bytes at
+//     a time (cp.async) from the row-major scale matrices into the 512-byte layout
+//     that tcgen05.cp spreads over tensor memory (row r at 16 (r % 32) + 4 (r / 32)).
+//     Each ring stage has its own scale columns in tensor memory, so a stage's copy
+//     never waits for another stage's MMAs.
+//   - Tiles are derived from expert_offsets by every CTA itself (a prefix sum in
+//     shared memory), so there is no tile list and no launch for one.
+// Every mbarrier wait is bounded (mbar_wait); on a timeout the kernel records the
+// error word, stops issuing, drains what it issued and frees TMEM.
+#include <cuda.h>
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
+#include "gemm_common.cuh"
 #include "kernels.h"
 #include "mx_common.cuh"
 #include "ptx.cuh"
@@ -14,90 +41,586 @@ namespace moe {
 
 namespace {
 
-__device__ __forceinline__ float e8m0(uint32_t c)
+using gemm::named_bar_or;
+using gemm::named_bar_sync;
+using gemm::silu_mul;
+
+constexpr int kBM = 128;                  // weight rows per tile (MMA M)
+constexpr int kBK = 128;                  // K elements per stage: one 128-byte swizzle row
+constexpr int kATile = kBM * kBK;         // bytes in shared memory (one per element)
+constexpr int kATxBytes = kATile / 2;     // an unpacking TMA load counts its packed bytes
+constexpr int kMaxExperts = 1024;
+constexpr int kScaleWarps = 2, kGatherWarps = 4, kEpiWarps = 8;
+constexpr int kScaleWarp0 = 2, kEpiWarp0 = 4, kGatherWarp0 = 12;
+constexpr int kMaxStages = 12;
+
+// Instruction descriptor of kind::mxf8f6f4: E2M1 A (code 5), E4M3 B (code 0), both
+// K-major, E8M0 scales; `kb` selects the scale byte of the K block, 0..3.
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N, int kb)
 {
-    return c == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(c ? c << 23 : 1u << 22);
+    return ((uint32_t)kb << 4) | (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(M >> 4) << 24) | ((uint32_t)kb << 29);
 }
 
-__device__ __forceinline__ float e4m3(uint32_t c)
+__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate)
 {
-    const uint32_t e = (c >> 3) & 15, m = c & 7;
-    float v = e ? __uint_as_float(((e + 120) << 23) | (m << 20)) : (float)m * 0.001953125f;
-    if ((c & 127) == 127) v = __uint_as_float(0x7FC00000u);
-    return c & 128 ? -v : v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
 }
 
-__device__ __forceinline__ float e2m1(uint32_t c)
+// Copies 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, the same 32
+// lanes' worth in every lane quarter.  Ordered before later MMAs of this thread.
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t smem)
 {
-    const uint32_t e = (c >> 1) & 3, m = c & 1;
-    const float v = e ? __uint_as_float(((e + 126) << 23) | (m << 22)) : (float)m * 0.5f;
-    return c & 8 ? -v : v;
+    // no swizzle; groups of 8 rows are 128 bytes apart
+    const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
+                       ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
-// The dot product of one row of a and one of w, block by block.
-__device__ float dot(const uint8_t* a, const uint8_t* sa, const uint8_t* w, const uint8_t* sw, int K)
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src)
 {
-    float acc = 0.f;
-    for (int b = 0; b < K / 32; ++b) {
-        float s = 0.f;
-        for (int i = 0; i < 16; ++i) {
-            const uint32_t q = w[b * 16 + i];
-            s = fmaf(e4m3(a[b * 32 + 2 * i]), e2m1(q & 15), s);
-            s = fmaf(e4m3(a[b * 32 + 2 * i + 1]), e2m1(q >> 4), s);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+template <int MODE, int NT>
+struct Cfg {
+    static constexpr int kThreads = MODE == 0 ? 512 : 384;
+    static constexpr int kBTile = NT * kBK;
+    static constexpr int kSfbCols = 4 * ((NT + 127) / 128);      // TMEM columns of B's scales
+    static constexpr int kSfCols = 4 + kSfbCols;
+    static constexpr int kSfBytes = kSfCols * 128;
+    static constexpr int kStageBytes = (kATile + kBTile + kSfBytes + 1023) & ~1023;
+    // epilogue staging: MODE 0: 8 warps x 2 x 8 columns x 32 lanes of fp32; MODE 1: 2
+    // groups x 2 x 8 token rows x 128 bf16
+    static constexpr int kStaging = MODE == 0 ? 16384 : 8192;
+    static constexpr int kTables = 2 * (kMaxExperts + 1) * 4 + 8 + 128;
+    static constexpr int kAux = 1024;
+    static constexpr int kFixed = 1024 + kStaging + kTables + kAux;
+    static constexpr int kStagesRaw = (232448 - kFixed) / kStageBytes;
+    static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
+    static constexpr int kNBuf = NT <= 64 ? 4 : 2;               // accumulators in flight
+    static constexpr int kSfCol0 = kNBuf * NT;                   // first scale column
+    static constexpr int kUsedCols = kSfCol0 + kStages * kSfCols;
+    static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
+    static constexpr int kGroupCols = NT / 2;                    // token columns per epilogue group
+    static constexpr int kGIters = (NT * 8 + kGatherWarps * 32 - 1) / (kGatherWarps * 32);
+    static constexpr int kSIters = (NT + kScaleWarps * 32 - 1) / (kScaleWarps * 32);
+    static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N tile");
+    static_assert(kStages >= 2 && kUsedCols <= 512 && kSmem <= 232448, "resources");
+};
+
+struct Aux {
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t tfull[4];
+    uint64_t tempty[4];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int warp_sum[16];
+};
+
+// One tile of a group: `rows` token rows from `row`, the feature block `fb` of `expert`.
+struct Unit {
+    int expert, fb, row, rows;
+};
+
+template <int MODE, int NT>
+__global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
+    mx_grouped_kernel(const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ CUtensorMap tm_a, const MxArgs g)
+{
+    using C = Cfg<MODE, NT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t* staging = ring + C::kStages * C::kStageBytes;
+    Aux* aux = reinterpret_cast<Aux*>(staging + C::kStaging);
+    static_assert(sizeof(Aux) <= C::kAux, "aux area");
+    int* first = reinterpret_cast<int*>(staging + C::kStaging + C::kAux);  // [E + 1] tiles before e
+    int* start = first + kMaxExperts + 1;                                  // [E + 1] rows before e
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::kStages; ++s) {
+            // the producer's expect_tx, one arrival per scale warp and per gather warp
+            mbar_init(&aux->full[s], 1 + kScaleWarps + (MODE == 0 ? kGatherWarps : 0));
+            mbar_init(&aux->empty[s], 1);
         }
-        acc = fmaf(s * e8m0(sa[b]), e8m0(sw[b]), acc);
+        for (int b = 0; b < C::kNBuf; ++b) {
+            mbar_init(&aux->tfull[b], 1);
+            mbar_init(&aux->tempty[b], kEpiWarps);
+        }
+        mbar_init(&aux->drain, 1);
+        aux->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tm_w);
+        if (MODE == 1) tma_prefetch_desc(&tm_a);
     }
-    return acc;
-}
-
-// One thread per output (feature f of row p); a warp holds one MX block of act.
-template <int MODE>
-__global__ void __launch_bounds__(128) mx_grouped_kernel(const MxArgs g)
-{
+    if (warp == 1) {
+        tmem_alloc(&aux->tmem_base, C::kTmemCols);
+        tmem_relinquish();
+    }
+    // The second product of the FFN (g.early) takes only act from the launch before it;
+    // expert_offsets, rows and weights were complete before that launch passed its own
+    // wait, so the tables and the first weight tiles need not wait for it.
+    if (!g.early) pdl_wait();
     pdl_launch_dependents();
-    pdl_wait();
-    const int p = blockIdx.y + blockIdx.z * gridDim.y, f = blockIdx.x * 128 + threadIdx.x;
-    if (p >= min(g.R, g.offsets[g.E])) return;
-    int lo = 0, hi = g.E;  // the expert of row p: the last e with offsets[e] <= p
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if (g.offsets[mid] <= p) lo = mid; else hi = mid;
+
+    // tiles before each expert (exclusive prefix sums), offsets clamped to 0 .. R and
+    // ascending, so that no offset leads outside the operands
+    {
+        constexpr int kPer = (kMaxExperts + C::kThreads - 1) / C::kThreads;
+        int tiles[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            tiles[i] = 0;
+            if (e < g.E) {
+                const int a = min(max(__ldcg(g.offsets + e), 0), g.R);
+                const int b = min(max(__ldcg(g.offsets + e + 1), a), g.R);
+                start[e] = a;
+                if (e == g.E - 1) start[g.E] = b;
+                tiles[i] = (b - a + NT - 1) / NT;
+            }
+            sum += tiles[i];
+        }
+        int incl = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) aux->warp_sum[warp] = incl;
+        tc_fence_before();
+        __syncthreads();
+        tc_fence_after();
+        int before = incl - sum;
+        for (int w = 0; w < warp; ++w) before += aux->warp_sum[w];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            if (e < g.E) first[e] = before;
+            before += tiles[i];
+            if (e == g.E - 1) first[g.E] = before;
+        }
+        __syncthreads();
     }
-    const int r = MODE == 2 ? p : g.rows[p];
-    const size_t arow = MODE == 0 ? r / g.k : p;
-    const uint8_t* a = g.a + arow * g.K;
-    const uint8_t* sa = g.a_scale + arow * (g.K / 32);
-    const size_t wrow = (size_t)lo * (MODE == 0 ? 2 * g.N : g.N) + f;
-    if (f >= g.N) return;
-    float v = dot(a, sa, g.w + wrow * (g.K / 2), g.w_scale + wrow * (g.K / 32), g.K);
-    if (MODE == 0) {
-        const size_t up = wrow + g.N;
-        const float u = dot(a, sa, g.w + up * (g.K / 2), g.w_scale + up * (g.K / 32), g.K);
-        v = v / (1.0f + expf(-v)) * u;
-        uint32_t m = __float_as_uint(v) & 0x7FFFFFFFu;
-        for (int o = 16; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const uint32_t code = mx::scale_code(m, mx::kEmaxE4M3);
-        const float q = v * mx::inverse_scale(min(code, 254u));
-        g.act[(size_t)p * g.N + f] = code == 255 ? 0x7F : (uint8_t)mx::e4m3x4(q, q, q, q);
-        if ((f & 31) == 0) g.act_scale[(size_t)p * (g.N / 32) + f / 32] = (uint8_t)code;
+    const uint32_t tmem_base = aux->tmem_base;
+    volatile int* abort_flag = &aux->abort;
+    auto flag_error = [&] {
+        atomicExch(g.err, kDeviceErrorMagic);
+        aux->abort = 1;
+    };
+
+    const int fbs = g.fb_count;
+    const int units = first[g.E] * fbs;
+    const int num_kt = g.K / kBK;
+    // unit u: experts in order; within one, feature block major and tile minor, so the
+    // tiles that share a weight block run at the same time on neighbouring CTAs and
+    // share it in L2.  A group of c rows in t tiles is cut evenly (to 16 rows).
+    auto decode = [&](int u) {
+        const int rest = u / fbs;
+        int lo = 0, hi = g.E;  // the last e with first[e] <= rest
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (first[mid] <= rest) lo = mid; else hi = mid;
+        }
+        const int local = u - first[lo] * fbs, count = first[lo + 1] - first[lo];
+        Unit t;
+        t.expert = lo;
+        t.fb = local / count;
+        const int rows = start[lo + 1] - start[lo];
+        const int per = ((rows + count - 1) / count + 15) & ~15;
+        const int at = (local % count) * per;
+        t.row = start[lo] + at;
+        t.rows = min(per, rows - at);
+        return t;
+    };
+    // first weight row of a unit's tile, of the [E * rows, K] weight matrix; MODE 0's up rows are
+    // N further on
+    auto weight_row = [&](const Unit& t) {
+        return MODE == 0 ? t.expert * 2 * g.N + t.fb * 64 : t.expert * g.N + t.fb * kBM;
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        if (lane == 0) {
+            const uint64_t pol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
+            int stage = 0, fills = 0;
+            uint32_t phase = 0;
+            bool ok = true, dep = !(MODE == 1 && g.early);
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+                const Unit t = decode(u);
+                const int row = weight_row(t);
+                for (int kt = 0; kt < num_kt; ++kt) {
+                    if (!mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag)) {
+                        flag_error();
+                        ok = false;
+                        break;
+                    }
+                    uint8_t* st = ring + stage * C::kStageBytes;
+                    uint64_t* bar = &aux->full[stage];
+                    mbar_arrive_expect_tx(bar, kATxBytes + (MODE == 1 ? C::kBTile : 0));
+                    tma_load_2d(st, &tm_w, bar, kt * kBK, row, pol);
+                    tma_load_2d(st + kATile / 2, &tm_w, bar, kt * kBK,
+                                row + (MODE == 0 ? g.N : kBM / 2), pol);
+                    if (MODE == 1) {
+                        if (!dep) {
+                            pdl_wait();
+                            dep = true;
+                        }
+                        tma_load_2d_nohint(st + kATile, &tm_a, bar, kt * kBK, t.row);
+                    }
+                    ++fills;
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!dep) pdl_wait();  // (no unit here) the grid still depends on it
+            if (!ok || *abort_flag) {
+                // let every TMA load already issued land before the CTA can exit
+                for (int s = 0; s < C::kStages; ++s) {
+                    const int n = fills > s ? (fills - s + C::kStages - 1) / C::kStages : 0;
+                    if (n > 0) {
+                        volatile int never = 0;
+                        mbar_wait(&aux->full[s], (uint32_t)((n - 1) & 1), &never, 500000000ull);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            int stage = 0, lu = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++lu) {
+                const Unit t = decode(u);
+                const int b = lu % C::kNBuf;
+                if (!mbar_wait(&aux->tempty[b], (uint32_t)((lu / C::kNBuf) & 1) ^ 1u, abort_flag)) {
+                    flag_error();
+                    break;
+                }
+                tc_fence_after();
+                const int n = (t.rows + 15) & ~15;
+                const uint32_t d = tmem_base + (uint32_t)(b * NT);
+                for (int kt = 0; kt < num_kt; ++kt) {
+                    if (!mbar_wait(&aux->full[stage], phase, abort_flag)) {
+                        flag_error();
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_smem();  // cp.async writes, read by the async proxy below
+                    tc_fence_after();
+                    const uint32_t sa = smem_u32(ring + stage * C::kStageBytes);
+                    const uint32_t sb = sa + kATile, sf = sb + C::kBTile;
+                    const uint32_t tsf = tmem_base + (uint32_t)(C::kSfCol0 + stage * C::kSfCols);
+                    scales_to_tmem(tsf, sf);
+#pragma unroll
+                    for (int i = 0; i < C::kSfbCols / 4; ++i)
+                        if (i * 128 < n) scales_to_tmem(tsf + 4 + 4 * i, sf + 512 * (1 + i));
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 32; ++kk)
+                        umma_mx(d, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32),
+                                idesc_mx(kBM, n, kk), tsf, tsf + 4, (kt | kk) ? 1u : 0u);
+                    umma_commit(&aux->empty[stage]);
+                    if (++stage == C::kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) umma_commit(&aux->tfull[b]);
+            }
+            // all MMAs and copies issued by this thread are complete before TMEM is freed
+            umma_commit(&aux->drain);
+            volatile int never = 0;
+            if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
+        }
+    } else if (warp < kEpiWarp0) {
+        // ------------------------------------------------------------ scales
+        // Thread i copies the scales of weight rows i and i + 64 and of token rows i, i + 64,
+        // ...  The copies arrive on the stage's barrier when they land.
+        const int i0 = threadIdx.x - kScaleWarp0 * 32;
+        const size_t ld = (size_t)g.K / 32;
+        if (MODE == 1 && g.early) pdl_wait();  // act's scales
+        auto place = [](int r) { return (uint32_t)((r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4); };
+        int q = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit t = decode(u);
+            const uint8_t *wsrc[2], *asrc[C::kSIters];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // MODE 1: the last block's rows may lie past N; theirs are never stored
+                const int row = MODE == 0 ? weight_row(t) + i * g.N + i0
+                                          : t.expert * g.N + min(t.fb * kBM + i * 64 + i0, g.N - 1);
+                wsrc[i] = g.w_scale + (size_t)row * ld;
+            }
+#pragma unroll
+            for (int i = 0; i < C::kSIters; ++i) {
+                const int j = i0 + i * 64;
+                asrc[i] = nullptr;
+                if (j < t.rows) {
+                    int r = t.row + j;
+                    if (MODE == 0) {
+                        r = g.rows[r];
+                        if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
+                        r /= g.k;
+                    }
+                    asrc[i] = g.a_scale + (size_t)r * ld;
+                }
+            }
+            for (int kt = 0; kt < num_kt; ++kt, ++q) {
+                const int stage = q % C::kStages;
+                const uint32_t phase = (uint32_t)((q / C::kStages) & 1);
+                if (!__all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag))) {
+                    if (lane == 0) flag_error();
+                    ok = false;
+                    break;
+                }
+                const uint32_t sf = smem_u32(ring + stage * C::kStageBytes + kATile + C::kBTile);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) cp_async_4(sf + place(i0 + i * 64), wsrc[i] + kt * 4);
+#pragma unroll
+                for (int i = 0; i < C::kSIters; ++i)
+                    if (asrc[i]) cp_async_4(sf + 512 + place(i0 + i * 64), asrc[i] + kt * 4);
+                cp_async_mbar_arrive(&aux->full[stage]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->full[stage]);
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();  // no copy is still in flight when the CTA exits
+    } else if (MODE == 0 && warp >= kGatherWarp0) {
+        // ------------------------------------------------------------ gather (MODE 0)
+        // Thread i copies the 16-byte chunks i, i + 128, ... of the tile's token rows (8 chunks a
+        // row), straight to their swizzled places.
+        const int i0 = threadIdx.x - kGatherWarp0 * 32;
+        const uint64_t pol = l2_policy_evict_last();  // token rows are read again per block
+        const uint8_t* src[C::kGIters];
+        int q = 0;
+        bool ok = true;
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit t = decode(u);
+#pragma unroll
+            for (int i = 0; i < C::kGIters; ++i) {
+                const int j = (i0 + i * 128) >> 3;
+                src[i] = nullptr;
+                if (j < t.rows) {
+                    int r = g.rows[t.row + j];
+                    if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
+                    src[i] = g.a + (size_t)(r / g.k) * g.K + (i0 & 7) * 16;
+                }
+            }
+            for (int kt = 0; kt < num_kt; ++kt, ++q) {
+                const int stage = q % C::kStages;
+                const uint32_t phase = (uint32_t)((q / C::kStages) & 1);
+                if (!__all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag))) {
+                    if (lane == 0) flag_error();
+                    ok = false;
+                    break;
+                }
+                const uint32_t sb = smem_u32(ring + stage * C::kStageBytes + kATile);
+#pragma unroll
+                for (int i = 0; i < C::kGIters; ++i) {
+                    const int c = i0 + i * 128, j = c >> 3;
+                    if (src[i])
+                        cp_async_16_hint(sb + j * 128 + (((c & 7) ^ (j & 7)) << 4), src[i] + kt * kBK, pol);
+                }
+                cp_async_mbar_arrive(&aux->full[stage]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->full[stage]);
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
     } else {
-        static_cast<__nv_bfloat16*>(g.y)[(size_t)r * g.N + f] = __float2bfloat16(v);
+        // ------------------------------------------------------------ epilogue
+        const int grp = (warp - kEpiWarp0) >> 2;     // token-column group
+        const int lq = warp & 3;                     // TMEM lane quarter
+        const int gt = (warp - kEpiWarp0 - grp * 4) * 32 + lane;
+        int lu = 0, chunk = 0;
+        for (int u = blockIdx.x; u < units; u += gridDim.x, ++lu) {
+            const Unit t = decode(u);
+            const int b = lu % C::kNBuf;
+            const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu / C::kNBuf) & 1), abort_flag);
+            if (!got) flag_error();
+            if (named_bar_or(1 + grp, 128, !got || *abort_flag)) break;  // same in all 4 warps
+            tc_fence_after();
+            const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * NT);
+            const int jbeg = grp * C::kGroupCols, jend = min(t.rows, jbeg + C::kGroupCols);
+            if constexpr (MODE == 0) {
+                // Lanes 0-63 hold gate rows, 64-127 the up rows of the same features.  Warps lq
+                // and lq ^ 2 exchange 4 of every 8 columns through shared memory: the gate
+                // warp finishes the first 4, the up warp the others.  A warp's 32 lanes are
+                // then one MX block of act for each of its columns.
+                const bool up = lq >= 2;
+                const int feature = t.fb * 64 + (lq & 1) * 32;
+                float* mine = reinterpret_cast<float*>(staging) + (warp - kEpiWarp0) * 512;
+                const float* other = reinterpret_cast<float*>(staging) + ((warp ^ 2) - kEpiWarp0) * 512;
+                for (int j0 = jbeg; j0 < jend; j0 += 8, ++chunk) {
+                    uint32_t v[8];
+                    tmem_ld8(acc + j0, v);
+                    tmem_ld_wait();
+                    const int buf = (chunk & 1) * 256;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        mine[buf + i * 32 + lane] = __uint_as_float(up ? v[i] : v[4 + i]);
+                    named_bar_sync(3 + grp * 2 + (lq & 1), 64);
+                    float a[4];
+                    uint32_t code[4], inv_bits = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float o = other[buf + i * 32 + lane];
+                        const float own = __uint_as_float(up ? v[4 + i] : v[i]);
+                        a[i] = up ? silu_mul(o, own) : silu_mul(own, o);
+                        const uint32_t m = __reduce_max_sync(0xffffffffu,
+                                                             __float_as_uint(a[i]) & 0x7FFFFFFFu);
+                        code[i] = mx::scale_code(m, mx::kEmaxE4M3);
+                        a[i] *= mx::inverse_scale(min(code[i], 254u));
+                    }
+                    (void)inv_bits;
+                    const uint32_t q4 = mx::e4m3x4(a[0], a[1], a[2], a[3]);
+                    const int j = j0 + (up ? 4 : 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (j + i < jend) {
+                            const size_t p = (size_t)(t.row + j + i);
+                            g.act[p * g.N + feature + lane] =
+                                code[i] == mx::kNanScale ? 0x7F : (uint8_t)(q4 >> (8 * i));
+                            if (lane == i)
+                                g.act_scale[p * (g.N / 32) + feature / 32] = (uint8_t)code[i];
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->tempty[b]);
+            } else {
+                // 1. drain this group's columns into registers as packed bf16 and hand them
+                //    back; 2. stage 8 token rows of 128 features at a time and store whole
+                //    row segments.  Two buffers, one barrier per chunk.
+                uint32_t pk[C::kGroupCols / 2];
+#pragma unroll
+                for (int c = 0; c < C::kGroupCols; c += 8) {
+                    if (jbeg + c < jend) {
+                        uint32_t v[8];
+                        tmem_ld8(acc + jbeg + c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; i += 2) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i]),
+                                                                           __uint_as_float(v[i + 1]));
+                            pk[(c + i) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->tempty[b]);
+                const int jj = gt >> 4, cc = gt & 15;
+                const int col = t.fb * kBM + cc * 8;
+#pragma unroll
+                for (int c = 0; c < C::kGroupCols; c += 8) {
+                    if (jbeg + c < jend) {
+                        uint8_t* buf = staging + (grp * 2 + (chunk & 1)) * 2048;
+#pragma unroll
+                        for (int r = 0; r < 8; ++r) {
+                            const uint32_t w = pk[(c + r) / 2];
+                            reinterpret_cast<uint16_t*>(buf + r * 256)[lq * 32 + lane] =
+                                (uint16_t)((r & 1) ? (w >> 16) : (w & 0xFFFFu));
+                        }
+                        named_bar_sync(1 + grp, 128);
+                        if (jbeg + c + jj < jend && col < g.N) {
+                            const int p = t.row + jbeg + c + jj;
+                            const uint4 val = *reinterpret_cast<const uint4*>(buf + jj * 256 + cc * 16);
+                            const int row = g.rows ? g.rows[p] : p;
+                            if (debug_in_range(row, 0, g.R, g.err))
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.y) +
+                                                          (size_t)row * g.N + col) = val;
+                        }
+                        ++chunk;
+                    }
+                }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, C::kTmemCols);
     }
 }
 
-template <int MODE>
-cudaError_t launch_mode(const MxArgs& g, cudaStream_t st)
+// ------------------------------------------------------------------ host side
+
+// E2M1 codes [rows, cols / 2]: a box of box_rows x 128 elements, unpacked to one byte slot
+// an element with the 128-byte swizzle.
+cudaError_t tmap_e2m1(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows)
 {
-    const int ry = g.R < 32768 ? g.R : 32768;
-    return launch_pdl(mx_grouped_kernel<MODE>, dim3((g.N + 127) / 128, ry, (g.R + ry - 1) / ry),
-                      dim3(128), 0, st, g);
+    gemm::EncodeTiledFn fn = gemm::get_encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols / 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kBK, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int MODE, int NT>
+cudaError_t launch_nt(const MxArgs& g, cudaStream_t st)
+{
+    using C = Cfg<MODE, NT>;
+    CUtensorMap tw, ta;
+    cudaError_t e = tmap_e2m1(&tw, g.w, (uint64_t)g.E * g.N * (MODE == 0 ? 2 : 1), (uint64_t)g.K, 64);
+    if (e == cudaSuccess)
+        e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, NT, kBK) : (ta = tw, e);
+    if (e != cudaSuccess) return e;
+    auto kern = mx_grouped_kernel<MODE, NT>;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(device_sms()), dim3(C::kThreads), C::kSmem, st, tw, ta, g);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
+{
+    if (most <= 16) return launch_nt<MODE, 16>(g, st);
+    if (most <= 32) return launch_nt<MODE, 32>(g, st);
+    if (most <= 64) return launch_nt<MODE, 64>(g, st);
+    return launch_nt<MODE, 128>(g, st);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_grouped(const MxArgs& g, int mode, cudaStream_t st)
+cudaError_t launch_mx_grouped(const MxArgs& args, int mode, cudaStream_t st)
 {
-    return mode == 0 ? launch_mode<0>(g, st) : mode == 1 ? launch_mode<1>(g, st) : launch_mode<2>(g, st);
+    MxArgs g = args;
+    // the most rows that one expert can have: a token picks an expert at most once
+    const int most = mode == 2 ? g.R : g.R / g.k;
+    g.early = mode == 1;
+    g.stream_weights = most <= 64;
+    g.fb_count = mode == 0 ? g.N / 64 : (g.N + kBM - 1) / kBM;
+    if (mode == 2) g.rows = nullptr;
+    return mode == 0 ? launch_mode<0>(g, most, st) : launch_mode<1>(g, most, st);
 }
 
 }  // namespace moe
