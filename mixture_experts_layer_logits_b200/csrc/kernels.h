@@ -266,6 +266,8 @@ struct MxArgs {
     int E, R, k, N, K;
     // set by launch_mx_grouped
     int fb_count;            // feature blocks of an expert
+    uint32_t fb_magic;       // for divisions by fb_count and by k
+    uint32_t k_magic;
     int early;               // only `a` comes from the launch before
     int stream_weights;      // weights are read once: evict first
 };

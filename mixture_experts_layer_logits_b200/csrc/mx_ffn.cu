@@ -55,11 +55,16 @@ constexpr int kScaleWarp0 = 2, kEpiWarp0 = 4, kGatherWarp0 = 12;
 constexpr int kMaxStages = 12;
 
 // Instruction descriptor of kind::mxf8f6f4: E2M1 A (code 5), E4M3 B (code 0), both
-// K-major, E8M0 scales; `kb` selects the scale byte of the K block, 0..3.
-__device__ __forceinline__ uint32_t idesc_mx(int M, int N, int kb)
+// K-major, E8M0 scales.
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N)
 {
-    return ((uint32_t)kb << 4) | (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) |
-           ((uint32_t)(M >> 4) << 24) | ((uint32_t)kb << 29);
+    return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
+}
+
+// Its bits that select the scale byte of K block kb, 0..3, for B and A.
+__device__ __forceinline__ constexpr uint32_t idesc_kb(int kb)
+{
+    return ((uint32_t)kb << 4) | ((uint32_t)kb << 29);
 }
 
 __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -74,19 +79,49 @@ __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint
         : "memory");
 }
 
-// Copies 512 bytes of scales (32 rows of 16 bytes) to 4 TMEM columns, the same 32
-// lanes' worth in every lane quarter.  Ordered before later MMAs of this thread.
-__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint32_t smem)
+// Shared-memory descriptor of 512 bytes of scales: 32 rows of 16 bytes, no swizzle,
+// groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem)
 {
-    // no swizzle; groups of 8 rows are 128 bytes apart
-    const uint64_t d = (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) |
-                       ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+    return (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
+           ((uint64_t)1 << 46);
+}
+
+// Copies them to 4 TMEM columns, the same 32 lanes' worth in every lane quarter.
+// Ordered before later MMAs of this thread.
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                 : "memory");
 }
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// One lane of a converged warp, the same one every time.  The loops of the TMA and
+// MMA warps run in all 32 lanes and only the issue is the elected lane's: the
+// descriptors then stay in uniform registers, which the tensor instructions take
+// their operands from (a loop inside `if (lane == 0)` took 60 cycles to issue one MMA).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// n / d and n % d for 0 <= n < 2^31 by a multiplication with m = floor(2^32 / d) + 1
+// (d = 1: m = 0).  The product can be one too large where n d is large; that is put right.
+__device__ __forceinline__ int div_by(int n, int d, uint32_t m)
+{
+    int q = d == 1 ? n : (int)__umulhi((uint32_t)n, m);
+    if (q * d > n) --q;
+    return q;
 }
 
 template <int MODE, int NT>
@@ -148,7 +183,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
     int* first = reinterpret_cast<int*>(staging + C::kStaging + C::kAux);  // [E + 1] tiles before e
     int* start = first + kMaxExperts + 1;                                  // [E + 1] rows before e
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
@@ -228,22 +263,33 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
     // unit u: experts in order; within one, feature block major and tile minor, so the
     // tiles that share a weight block run at the same time on neighbouring CTAs and
     // share it in L2.  A group of c rows in t tiles is cut evenly (to 16 rows).
-    auto decode = [&](int u) {
-        const int rest = u / fbs;
-        int lo = 0, hi = g.E;  // the last e with first[e] <= rest
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (first[mid] <= rest) lo = mid; else hi = mid;
+    // All 32 lanes decode together; `e` is the expert of this warp's unit before (a
+    // CTA's units ascend, so the search starts there, 32 experts at a time).
+    auto decode = [&](int u, int& e) {
+        const int rest = div_by(u, fbs, g.fb_magic);
+        for (;;) {  // to the last e with first[e] <= rest
+            const int at = e + 1 + lane;
+            const uint32_t past = __ballot_sync(0xffffffffu, at > g.E || first[min(at, g.E)] > rest);
+            if (past) {
+                e += __ffs(past) - 1;
+                break;
+            }
+            e += 32;
         }
-        const int local = u - first[lo] * fbs, count = first[lo + 1] - first[lo];
+        const int local = u - first[e] * fbs, count = first[e + 1] - first[e];
+        const int rows = start[e + 1] - start[e];
         Unit t;
-        t.expert = lo;
-        t.fb = local / count;
-        const int rows = start[lo + 1] - start[lo];
-        const int per = ((rows + count - 1) / count + 15) & ~15;
-        const int at = (local % count) * per;
-        t.row = start[lo] + at;
-        t.rows = min(per, rows - at);
+        t.expert = e;
+        t.fb = local;
+        t.row = start[e];
+        t.rows = rows;
+        if (count > 1) {
+            const int per = ((rows + count - 1) / count + 15) & ~15;
+            t.fb = local / count;
+            const int at = (local - t.fb * count) * per;
+            t.row += at;
+            t.rows = min(per, rows - at);
+        }
         return t;
     };
     // first weight row of a unit's tile, of the [E * rows, K] weight matrix; MODE 0's up rows are
@@ -254,100 +300,99 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        if (lane == 0) {
-            const uint64_t pol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
-            int stage = 0, fills = 0;
-            uint32_t phase = 0;
-            bool ok = true, dep = !(MODE == 1 && g.early);
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-                const Unit t = decode(u);
-                const int row = weight_row(t);
-                for (int kt = 0; kt < num_kt; ++kt) {
-                    if (!mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag)) {
-                        flag_error();
-                        ok = false;
-                        break;
-                    }
-                    uint8_t* st = ring + stage * C::kStageBytes;
-                    uint64_t* bar = &aux->full[stage];
+        const uint64_t pol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
+        int stage = 0, fills = 0, e = 0;
+        uint32_t phase = 0;
+        bool ok = true, dep = !(MODE == 1 && g.early);
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+            const Unit t = decode(u, e);
+            const int row = weight_row(t);
+            for (int kt = 0; kt < num_kt; ++kt) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                uint8_t* st = ring + stage * C::kStageBytes;
+                uint64_t* bar = &aux->full[stage];
+                if (elect_one()) {
                     mbar_arrive_expect_tx(bar, kATxBytes + (MODE == 1 ? C::kBTile : 0));
                     tma_load_2d(st, &tm_w, bar, kt * kBK, row, pol);
                     tma_load_2d(st + kATile / 2, &tm_w, bar, kt * kBK,
                                 row + (MODE == 0 ? g.N : kBM / 2), pol);
                     if (MODE == 1) {
-                        if (!dep) {
-                            pdl_wait();
-                            dep = true;
-                        }
+                        if (!dep) pdl_wait();
                         tma_load_2d_nohint(st + kATile, &tm_a, bar, kt * kBK, t.row);
                     }
-                    ++fills;
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                __syncwarp();
+                dep = true;
+                ++fills;
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            if (!dep) pdl_wait();  // (no unit here) the grid still depends on it
-            if (!ok || *abort_flag) {
-                // let every TMA load already issued land before the CTA can exit
-                for (int s = 0; s < C::kStages; ++s) {
-                    const int n = fills > s ? (fills - s + C::kStages - 1) / C::kStages : 0;
-                    if (n > 0) {
-                        volatile int never = 0;
-                        mbar_wait(&aux->full[s], (uint32_t)((n - 1) & 1), &never, 500000000ull);
-                    }
+        }
+        if (!dep) pdl_wait();  // (no unit here) the grid still depends on it
+        if (!ok || *abort_flag) {
+            if (lane == 0) flag_error();
+            // let every TMA load already issued land before the CTA can exit
+            for (int s = 0; s < C::kStages; ++s) {
+                const int n = fills > s ? (fills - s + C::kStages - 1) / C::kStages : 0;
+                if (n > 0) {
+                    volatile int never = 0;
+                    mbar_wait(&aux->full[s], (uint32_t)((n - 1) & 1), &never, 500000000ull);
                 }
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            int stage = 0, lu = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++lu) {
-                const Unit t = decode(u);
-                const int b = lu % C::kNBuf;
-                if (!mbar_wait(&aux->tempty[b], (uint32_t)((lu / C::kNBuf) & 1) ^ 1u, abort_flag)) {
-                    flag_error();
-                    break;
-                }
+        int stage = 0, lu = 0, e = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t ring0 = smem_u32(ring);
+        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++lu) {
+            const Unit t = decode(u, e);
+            const int b = lu % C::kNBuf;
+            ok = __all_sync(0xffffffffu, mbar_wait(&aux->tempty[b], (uint32_t)((lu / C::kNBuf) & 1) ^ 1u,
+                                                   abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const int n = (t.rows + 15) & ~15;
+            const uint32_t d = tmem_base + (uint32_t)(b * NT), idesc = idesc_mx(kBM, n);
+            for (int kt = 0; kt < num_kt; ++kt) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&aux->full[stage], phase, abort_flag));
+                if (!ok) break;
                 tc_fence_after();
-                const int n = (t.rows + 15) & ~15;
-                const uint32_t d = tmem_base + (uint32_t)(b * NT);
-                for (int kt = 0; kt < num_kt; ++kt) {
-                    if (!mbar_wait(&aux->full[stage], phase, abort_flag)) {
-                        flag_error();
-                        ok = false;
-                        break;
-                    }
+                const uint32_t sa = ring0 + stage * C::kStageBytes;
+                const uint32_t sb = sa + kATile, sf = sb + C::kBTile;
+                const uint32_t tsf = tmem_base + (uint32_t)(C::kSfCol0 + stage * C::kSfCols);
+                const uint64_t da = umma_desc_sw128(sa), db = umma_desc_sw128(sb);
+                const uint64_t ds = scale_desc(sf);
+                if (elect_one()) {
                     fence_proxy_async_smem();  // cp.async writes, read by the async proxy below
-                    tc_fence_after();
-                    const uint32_t sa = smem_u32(ring + stage * C::kStageBytes);
-                    const uint32_t sb = sa + kATile, sf = sb + C::kBTile;
-                    const uint32_t tsf = tmem_base + (uint32_t)(C::kSfCol0 + stage * C::kSfCols);
-                    scales_to_tmem(tsf, sf);
+                    scales_to_tmem(tsf, ds);
 #pragma unroll
                     for (int i = 0; i < C::kSfbCols / 4; ++i)
-                        if (i * 128 < n) scales_to_tmem(tsf + 4 + 4 * i, sf + 512 * (1 + i));
+                        if (i * 128 < n) scales_to_tmem(tsf + 4 + 4 * i, ds + (512 >> 4) * (1 + i));
 #pragma unroll
-                    for (int kk = 0; kk < kBK / 32; ++kk)
-                        umma_mx(d, umma_desc_sw128(sa + kk * 32), umma_desc_sw128(sb + kk * 32),
-                                idesc_mx(kBM, n, kk), tsf, tsf + 4, (kt | kk) ? 1u : 0u);
+                    for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along K
+                        umma_mx(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
+                                (kt | kk) ? 1u : 0u);
                     umma_commit(&aux->empty[stage]);
-                    if (++stage == C::kStages) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    if (kt + 1 == num_kt) umma_commit(&aux->tfull[b]);
                 }
-                if (ok) umma_commit(&aux->tfull[b]);
+                __syncwarp();
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            // all MMAs and copies issued by this thread are complete before TMEM is freed
-            umma_commit(&aux->drain);
-            volatile int never = 0;
-            if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
         }
+        if (!ok && lane == 0) flag_error();
+        // all MMAs and copies issued by this warp are complete before TMEM is freed
+        if (elect_one()) umma_commit(&aux->drain);
+        __syncwarp();
+        volatile int never = 0;
+        if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
     } else if (warp < kEpiWarp0) {
         // ------------------------------------------------------------ scales
         // Thread i copies the scales of weight rows i and i + 64 and of token rows i, i + 64,
@@ -356,10 +401,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         const size_t ld = (size_t)g.K / 32;
         if (MODE == 1 && g.early) pdl_wait();  // act's scales
         auto place = [](int r) { return (uint32_t)((r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4); };
-        int q = 0;
+        int q = 0, e = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Unit t = decode(u);
+            const Unit t = decode(u, e);
             const uint8_t *wsrc[2], *asrc[C::kSIters];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -377,7 +422,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                     if (MODE == 0) {
                         r = g.rows[r];
                         if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
-                        r /= g.k;
+                        r = div_by(r, g.k, g.k_magic);
                     }
                     asrc[i] = g.a_scale + (size_t)r * ld;
                 }
@@ -410,10 +455,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         const int i0 = threadIdx.x - kGatherWarp0 * 32;
         const uint64_t pol = l2_policy_evict_last();  // token rows are read again per block
         const uint8_t* src[C::kGIters];
-        int q = 0;
+        int q = 0, e = 0;
         bool ok = true;
         for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Unit t = decode(u);
+            const Unit t = decode(u, e);
 #pragma unroll
             for (int i = 0; i < C::kGIters; ++i) {
                 const int j = (i0 + i * 128) >> 3;
@@ -421,7 +466,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                 if (j < t.rows) {
                     int r = g.rows[t.row + j];
                     if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
-                    src[i] = g.a + (size_t)(r / g.k) * g.K + (i0 & 7) * 16;
+                    src[i] = g.a + (size_t)div_by(r, g.k, g.k_magic) * g.K + (i0 & 7) * 16;
                 }
             }
             for (int kt = 0; kt < num_kt; ++kt, ++q) {
@@ -451,9 +496,9 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         const int grp = (warp - kEpiWarp0) >> 2;     // token-column group
         const int lq = warp & 3;                     // TMEM lane quarter
         const int gt = (warp - kEpiWarp0 - grp * 4) * 32 + lane;
-        int lu = 0, chunk = 0;
+        int lu = 0, chunk = 0, e = 0;
         for (int u = blockIdx.x; u < units; u += gridDim.x, ++lu) {
-            const Unit t = decode(u);
+            const Unit t = decode(u, e);
             const int b = lu % C::kNBuf;
             const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu / C::kNBuf) & 1), abort_flag);
             if (!got) flag_error();
@@ -480,7 +525,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                         mine[buf + i * 32 + lane] = __uint_as_float(up ? v[i] : v[4 + i]);
                     named_bar_sync(3 + grp * 2 + (lq & 1), 64);
                     float a[4];
-                    uint32_t code[4], inv_bits = 0;
+                    uint32_t code[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float o = other[buf + i * 32 + lane];
@@ -491,7 +536,6 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                         code[i] = mx::scale_code(m, mx::kEmaxE4M3);
                         a[i] *= mx::inverse_scale(min(code[i], 254u));
                     }
-                    (void)inv_bits;
                     const uint32_t q4 = mx::e4m3x4(a[0], a[1], a[2], a[3]);
                     const int j = j0 + (up ? 4 : 0);
 #pragma unroll
@@ -619,7 +663,13 @@ cudaError_t launch_mx_grouped(const MxArgs& args, int mode, cudaStream_t st)
     g.early = mode == 1;
     g.stream_weights = most <= 64;
     g.fb_count = mode == 0 ? g.N / 64 : (g.N + kBM - 1) / kBM;
-    if (mode == 2) g.rows = nullptr;
+    auto magic = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (unsigned)d + 1) : 0u; };
+    g.fb_magic = magic(g.fb_count);
+    if (mode == 2) {
+        g.rows = nullptr;
+        g.k = 1;
+    }
+    g.k_magic = magic(g.k);
     return mode == 0 ? launch_mode<0>(g, most, st) : launch_mode<1>(g, most, st);
 }
 
