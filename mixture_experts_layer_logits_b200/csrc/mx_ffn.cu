@@ -67,16 +67,27 @@ __device__ __forceinline__ constexpr uint32_t idesc_kb(int kb)
     return ((uint32_t)kb << 4) | ((uint32_t)kb << 29);
 }
 
+// CG: CTAs that work on one MMA (cta_group::1 or ::2).
+template <int CG>
 __device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                         uint32_t sfa, uint32_t sfb, uint32_t accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], "
-        "[%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-        : "memory");
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
 }
 
 // Shared-memory descriptor of 512 bytes of scales: 32 rows of 16 bytes, no swizzle,
@@ -89,10 +100,109 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem)
 
 // Copies them to 4 TMEM columns, the same 32 lanes' worth in every lane quarter.
 // Ordered before later MMAs of this thread.
+// With CG = 2 each of the two CTAs copies from its own shared memory to its own TMEM.
+template <int CG>
 __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                 : "memory");
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+}
+
+// Arrive on `bar` (with CG = 2: on the barrier at this address in both CTAs) when every
+// tensor instruction issued so far by this thread is done.
+template <int CG>
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    if constexpr (CG == 1)
+        umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+            "[%0], %1;" ::"r"(smem_u32(bar)),
+            "h"((uint16_t)3)
+            : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_acquire(uint32_t* dst, uint32_t cols)
+{
+    if constexpr (CG == 1) {
+        tmem_alloc(dst, cols);
+        tmem_relinquish();
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(dst)),
+                     "r"(cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+}
+
+template <int CG>
+__device__ __forceinline__ void tmem_release(uint32_t taddr, uint32_t cols)
+{
+    if constexpr (CG == 1)
+        tmem_dealloc(taddr, cols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(cols)
+                     : "memory");
+}
+
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\t"
+        "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Arrive on the barrier that lies at this address in CTA 0 of the cluster.  It carries
+// only the fact.  What it stands for is a CTA's own shared memory, complete before the
+// arriving thread saw its own barrier (TMA tiles, and scales whose writers fenced the
+// async proxy), which the tensor core of that CTA's SM reads, or its own TMEM, read out
+// before tcgen05.wait::ld; so the default release (CTA scope) is enough.  A release at
+// cluster scope waits for the L2: 1200 cycles a stage, prefill 2.66 ms instead of 1.56.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
+        "mapa.shared::cluster.u32 a, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
+
+// mbar_wait for a barrier that the other CTA of the cluster arrives on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
+                                                  volatile int* abort)
+{
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((n & 255u) == 0) {
+            if (*abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (!t0) t0 = t;
+            if (t - t0 > 2000000000ull) return false;
+        }
+    }
 }
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src)
@@ -124,10 +234,12 @@ __device__ __forceinline__ int div_by(int n, int d, uint32_t m)
     return q;
 }
 
-template <int MODE, int NT>
+// NT: the most token rows of a tile (the MMA's N).
+template <int MODE, int NT, int CG>
 struct Cfg {
     static constexpr int kThreads = MODE == 0 ? 512 : 384;
-    static constexpr int kBTile = NT * kBK;
+    static constexpr int kBRows = NT / CG;                       // token rows in one CTA's B tile
+    static constexpr int kBTile = kBRows * kBK;
     static constexpr int kSfbCols = 4 * ((NT + 127) / 128);      // TMEM columns of B's scales
     static constexpr int kSfCols = 4 + kSfbCols;
     static constexpr int kSfBytes = kSfCols * 128;
@@ -138,16 +250,19 @@ struct Cfg {
     static constexpr int kTables = 2 * (kMaxExperts + 1) * 4 + 8 + 128;
     static constexpr int kAux = 1024;
     static constexpr int kFixed = 1024 + kStaging + kTables + kAux;
-    static constexpr int kStagesRaw = (232448 - kFixed) / kStageBytes;
-    static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
-    static constexpr int kSmem = kFixed + kStages * kStageBytes;
     static constexpr int kNBuf = NT <= 64 ? 4 : 2;               // accumulators in flight
     static constexpr int kSfCol0 = kNBuf * NT;                   // first scale column
+    static constexpr int kStagesSmem = (232448 - kFixed) / kStageBytes;
+    static constexpr int kStagesTmem = (512 - kSfCol0) / kSfCols;
+    static constexpr int kStagesRaw = kStagesSmem < kStagesTmem ? kStagesSmem : kStagesTmem;
+    static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
     static constexpr int kUsedCols = kSfCol0 + kStages * kSfCols;
     static constexpr int kTmemCols = kUsedCols <= 128 ? 128 : kUsedCols <= 256 ? 256 : 512;
     static constexpr int kGroupCols = NT / 2;                    // token columns per epilogue group
-    static constexpr int kGIters = (NT * 8 + kGatherWarps * 32 - 1) / (kGatherWarps * 32);
+    static constexpr int kGIters = (kBRows * 8 + kGatherWarps * 32 - 1) / (kGatherWarps * 32);
     static constexpr int kSIters = (NT + kScaleWarps * 32 - 1) / (kScaleWarps * 32);
+    static constexpr int kFeatures = CG * (MODE == 0 ? 64 : 128);  // output features per unit
     static_assert(NT % 16 == 0 && NT >= 16 && NT <= 256, "MMA N tile");
     static_assert(kStages >= 2 && kUsedCols <= 512 && kSmem <= 232448, "resources");
 };
@@ -155,6 +270,7 @@ struct Cfg {
 struct Aux {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
+    uint64_t peer_full[kMaxStages];  // CG = 2: the second CTA's stage is full too
     uint64_t tfull[4];
     uint64_t tempty[4];
     uint64_t drain;
@@ -168,12 +284,12 @@ struct Unit {
     int expert, fb, row, rows;
 };
 
-template <int MODE, int NT>
-__global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
+template <int MODE, int NT, int CG>
+__global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
     mx_grouped_kernel(const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ CUtensorMap tm_a, const MxArgs g)
 {
-    using C = Cfg<MODE, NT>;
+    using C = Cfg<MODE, NT, CG>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -190,10 +306,11 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
             // the producer's expect_tx, one arrival per scale warp and per gather warp
             mbar_init(&aux->full[s], 1 + kScaleWarps + (MODE == 0 ? kGatherWarps : 0));
             mbar_init(&aux->empty[s], 1);
+            mbar_init(&aux->peer_full[s], 1);
         }
         for (int b = 0; b < C::kNBuf; ++b) {
             mbar_init(&aux->tfull[b], 1);
-            mbar_init(&aux->tempty[b], kEpiWarps);
+            mbar_init(&aux->tempty[b], CG * kEpiWarps);
         }
         mbar_init(&aux->drain, 1);
         aux->abort = 0;
@@ -202,8 +319,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         if (MODE == 1) tma_prefetch_desc(&tm_a);
     }
     if (warp == 1) {
-        tmem_alloc(&aux->tmem_base, C::kTmemCols);
-        tmem_relinquish();
+        tmem_acquire<CG>(&aux->tmem_base, C::kTmemCols);
     }
     // The second product of the FFN (g.early) takes only act from the launch before it;
     // expert_offsets, rows and weights were complete before that launch passed its own
@@ -248,8 +364,13 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
             before += tiles[i];
             if (e == g.E - 1) first[g.E] = before;
         }
-        __syncthreads();
+        if constexpr (CG == 2)
+            cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
+        else
+            __syncthreads();
     }
+    const uint32_t rank = CG == 2 ? cluster_rank() : 0;
+    const int unit0 = (int)blockIdx.x / CG, stride = (int)gridDim.x / CG;
     const uint32_t tmem_base = aux->tmem_base;
     volatile int* abort_flag = &aux->abort;
     auto flag_error = [&] {
@@ -292,11 +413,20 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         }
         return t;
     };
-    // first weight row of a unit's tile, of the [E * rows, K] weight matrix; MODE 0's up rows are
-    // N further on
-    auto weight_row = [&](const Unit& t) {
-        return MODE == 0 ? t.expert * 2 * g.N + t.fb * 64 : t.expert * g.N + t.fb * kBM;
+    // first output feature of this CTA's part of a unit
+    auto first_feature = [&](const Unit& t) {
+        return t.fb * C::kFeatures + (int)rank * (C::kFeatures / CG);
     };
+    // first weight row of its tile, of the [E * rows, K] weight matrix; MODE 0's up rows
+    // are N further on.  MODE 1: a pair's second tile may begin past N; it then
+    // reads the first instead, and none of it is stored.
+    auto weight_row = [&](const Unit& t) {
+        const int f = first_feature(t);
+        return MODE == 0 ? t.expert * 2 * g.N + f : t.expert * g.N + (f < g.N ? f : 0);
+    };
+    // the MMA's N, and the first of this CTA's token rows in the tile
+    auto padded = [](int rows) { return (rows + 15) & ~15; };
+    auto first_token = [&](const Unit& t) { return CG == 2 ? (int)rank * (padded(t.rows) / 2) : 0; };
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
@@ -304,7 +434,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         int stage = 0, fills = 0, e = 0;
         uint32_t phase = 0;
         bool ok = true, dep = !(MODE == 1 && g.early);
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = unit0; u < units && ok; u += stride) {
             const Unit t = decode(u, e);
             const int row = weight_row(t);
             for (int kt = 0; kt < num_kt; ++kt) {
@@ -319,7 +449,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                                 row + (MODE == 0 ? g.N : kBM / 2), pol);
                     if (MODE == 1) {
                         if (!dep) pdl_wait();
-                        tma_load_2d_nohint(st + kATile, &tm_a, bar, kt * kBK, t.row);
+                        tma_load_2d_nohint(st + kATile, &tm_a, bar, kt * kBK, t.row + first_token(t));
                     }
                 }
                 __syncwarp();
@@ -343,23 +473,48 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                 }
             }
         }
+    } else if (warp == 1 && CG == 2 && rank == 1) {
+        // ------------------------------------------------------------ relay (second CTA)
+        // CTA 0 issues the MMAs of both; tell it when a stage of this CTA is full.
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int u = unit0; u < units && ok; u += stride) {
+            for (int kt = 0; kt < num_kt; ++kt) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&aux->full[stage], phase, abort_flag));
+                if (!ok) break;
+                if (elect_one()) {
+                    fence_proxy_async_smem();
+                    arrive_leader(&aux->peer_full[stage]);
+                }
+                __syncwarp();
+                if (++stage == C::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) flag_error();
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         int stage = 0, lu = 0, e = 0;
         uint32_t phase = 0;
         bool ok = true;
         const uint32_t ring0 = smem_u32(ring);
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x, ++lu) {
+        for (int u = unit0; u < units && ok; u += stride, ++lu) {
             const Unit t = decode(u, e);
             const int b = lu % C::kNBuf;
-            ok = __all_sync(0xffffffffu, mbar_wait(&aux->tempty[b], (uint32_t)((lu / C::kNBuf) & 1) ^ 1u,
-                                                   abort_flag));
+            const uint32_t bphase = (uint32_t)((lu / C::kNBuf) & 1) ^ 1u;
+            ok = __all_sync(0xffffffffu, CG == 2 ? mbar_wait_cluster(&aux->tempty[b], bphase, abort_flag)
+                                                 : mbar_wait(&aux->tempty[b], bphase, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const int n = (t.rows + 15) & ~15;
-            const uint32_t d = tmem_base + (uint32_t)(b * NT), idesc = idesc_mx(kBM, n);
+            const int n = padded(t.rows);
+            const uint32_t d = tmem_base + (uint32_t)(b * NT), idesc = idesc_mx(CG * kBM, n);
             for (int kt = 0; kt < num_kt; ++kt) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&aux->full[stage], phase, abort_flag));
+                ok = __all_sync(0xffffffffu,
+                                mbar_wait(&aux->full[stage], phase, abort_flag) &&
+                                    (CG == 1 || mbar_wait_cluster(&aux->peer_full[stage], phase, abort_flag)));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = ring0 + stage * C::kStageBytes;
@@ -369,16 +524,16 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                 const uint64_t ds = scale_desc(sf);
                 if (elect_one()) {
                     fence_proxy_async_smem();  // cp.async writes, read by the async proxy below
-                    scales_to_tmem(tsf, ds);
+                    scales_to_tmem<CG>(tsf, ds);
 #pragma unroll
                     for (int i = 0; i < C::kSfbCols / 4; ++i)
-                        if (i * 128 < n) scales_to_tmem(tsf + 4 + 4 * i, ds + (512 >> 4) * (1 + i));
+                        if (i * 128 < n) scales_to_tmem<CG>(tsf + 4 + 4 * i, ds + (512 >> 4) * (1 + i));
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along K
-                        umma_mx(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
-                                (kt | kk) ? 1u : 0u);
-                    umma_commit(&aux->empty[stage]);
-                    if (kt + 1 == num_kt) umma_commit(&aux->tfull[b]);
+                        umma_mx<CG>(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
+                                    (kt | kk) ? 1u : 0u);
+                    commit<CG>(&aux->empty[stage]);
+                    if (kt + 1 == num_kt) commit<CG>(&aux->tfull[b]);
                 }
                 __syncwarp();
                 if (++stage == C::kStages) {
@@ -389,65 +544,151 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         }
         if (!ok && lane == 0) flag_error();
         // all MMAs and copies issued by this warp are complete before TMEM is freed
-        if (elect_one()) umma_commit(&aux->drain);
+        if (elect_one()) commit<CG>(&aux->drain);
         __syncwarp();
         volatile int never = 0;
         if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
     } else if (warp < kEpiWarp0) {
         // ------------------------------------------------------------ scales
-        // Thread i copies the scales of weight rows i and i + 64 and of token rows i, i + 64,
-        // ...  The copies arrive on the stage's barrier when they land.
+        // Thread i handles weight rows i and i + 64 and token rows i, i + 64, ... of a tile; a
+        // row's 4 bytes of a K tile go to place(row) of the stage.
         const int i0 = threadIdx.x - kScaleWarp0 * 32;
         const size_t ld = (size_t)g.K / 32;
         if (MODE == 1 && g.early) pdl_wait();  // act's scales
         auto place = [](int r) { return (uint32_t)((r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4); };
+        constexpr int kRows = 2 + C::kSIters;
+        // index of token row j of the tile (0 past its end, where any scale will do)
+        auto token_row = [&](const Unit& t, int j) {
+            int r = t.row + min(j, t.rows - 1);
+            if (MODE == 0) {
+                r = g.rows[r];
+                if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
+            }
+            return r;
+        };
+        auto weight_src = [&](const Unit& t, int i) {
+            // MODE 1: the last block's rows may lie past N; theirs are never stored
+            const int row = MODE == 0 ? weight_row(t) + i * g.N + i0
+                                      : t.expert * g.N + min(first_feature(t) + i * 64 + i0, g.N - 1);
+            return g.w_scale + (size_t)row * ld;
+        };
+        auto token_src = [&](int r) {
+            return g.a_scale + (size_t)(MODE == 0 ? div_by(r, g.k, g.k_magic) : r) * ld;
+        };
         int q = 0, e = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
-            const Unit t = decode(u, e);
-            const uint8_t *wsrc[2], *asrc[C::kSIters];
+        auto wait_empty = [&](int stage) {
+            const uint32_t phase = (uint32_t)((q / C::kStages) & 1);
+            ok = __all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
+            if (!ok && lane == 0) flag_error();
+            return ok;
+        };
+        if constexpr (CG == 1) {
+            // Few token rows, many stages in flight: 4-byte cp.async copies, which arrive on the
+            // stage's barrier when they land.
+            for (int u = unit0; u < units && ok; u += stride) {
+                const Unit t = decode(u, e);
+                const uint8_t* src[kRows];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                // MODE 1: the last block's rows may lie past N; theirs are never stored
-                const int row = MODE == 0 ? weight_row(t) + i * g.N + i0
-                                          : t.expert * g.N + min(t.fb * kBM + i * 64 + i0, g.N - 1);
-                wsrc[i] = g.w_scale + (size_t)row * ld;
-            }
-#pragma unroll
-            for (int i = 0; i < C::kSIters; ++i) {
-                const int j = i0 + i * 64;
-                asrc[i] = nullptr;
-                if (j < t.rows) {
-                    int r = t.row + j;
-                    if (MODE == 0) {
-                        r = g.rows[r];
-                        if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
-                        r = div_by(r, g.k, g.k_magic);
-                    }
-                    asrc[i] = g.a_scale + (size_t)r * ld;
-                }
-            }
-            for (int kt = 0; kt < num_kt; ++kt, ++q) {
-                const int stage = q % C::kStages;
-                const uint32_t phase = (uint32_t)((q / C::kStages) & 1);
-                if (!__all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag))) {
-                    if (lane == 0) flag_error();
-                    ok = false;
-                    break;
-                }
-                const uint32_t sf = smem_u32(ring + stage * C::kStageBytes + kATile + C::kBTile);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) cp_async_4(sf + place(i0 + i * 64), wsrc[i] + kt * 4);
+                for (int i = 0; i < 2; ++i) src[i] = weight_src(t, i);
 #pragma unroll
                 for (int i = 0; i < C::kSIters; ++i)
-                    if (asrc[i]) cp_async_4(sf + 512 + place(i0 + i * 64), asrc[i] + kt * 4);
-                cp_async_mbar_arrive(&aux->full[stage]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&aux->full[stage]);
+                    src[2 + i] = i0 + i * 64 < t.rows ? token_src(token_row(t, i0 + i * 64)) : nullptr;
+                for (int kt = 0; kt < num_kt; ++kt, ++q) {
+                    const int stage = q % C::kStages;
+                    if (!wait_empty(stage)) break;
+                    const uint32_t sf = smem_u32(ring + stage * C::kStageBytes + kATile + C::kBTile);
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+                        if (i < 2 || src[i])
+                            cp_async_4(sf + (i < 2 ? place(i0 + i * 64) : 512 + place(i0 + (i - 2) * 64)),
+                                       src[i] + kt * 4);
+                    cp_async_mbar_arrive(&aux->full[stage]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&aux->full[stage]);
+                }
+            }
+            cp_async_commit();
+            cp_async_wait<0>();  // no copy is still in flight when the CTA exits
+        } else {
+            // Many token rows: a 4-byte copy is one L1 line lookup a row and K tile, which
+            // competes with the gather.  So rows are read 4 K tiles at a time (16 bytes where
+            // the row pitch allows it), one group ahead, and stored from registers.
+            const int align = (int)(ld & 15);  // 0: 16-byte rows, 8: 8-byte, else 4-byte
+            auto load = [&](uint32_t (&w)[4], const uint8_t* p, int kt) {
+                p += kt * 4;
+                if (align == 0) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+                    w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                } else if (align == 8) {
+                    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+                    w[0] = v.x, w[1] = v.y;
+                    if (kt + 2 < num_kt) {
+                        const uint2 x = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+                        w[2] = x.x, w[3] = x.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (kt + j < num_kt) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+                }
+            };
+            uint32_t cur[kRows][4], nxt[kRows][4];
+            const uint8_t* src[kRows];
+            int tok[C::kSIters];
+            Unit t = {};
+            if (unit0 < units) {
+                t = decode(unit0, e);
+#pragma unroll
+                for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(t, i0 + i * 64);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    src[i] = i < 2 ? weight_src(t, i) : token_src(tok[i - 2]);
+                    load(cur[i], src[i], 0);
+                }
+            }
+            for (int u = unit0; u < units && ok; u += stride) {
+                const bool more = u + stride < units;
+                if (more) {  // the next unit's rows, wanted at the end of this one
+                    t = decode(u + stride, e);
+#pragma unroll
+                    for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(t, i0 + i * 64);
+                }
+                for (int kt = 0; kt < num_kt && ok; kt += 4) {
+                    if (kt + 4 < num_kt) {
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i) load(nxt[i], src[i], kt + 4);
+                    } else if (more) {
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i) {
+                            src[i] = i < 2 ? weight_src(t, i) : token_src(tok[i - 2]);
+                            load(nxt[i], src[i], 0);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (kt + j >= num_kt) break;
+                        const int stage = q % C::kStages;
+                        if (!wait_empty(stage)) break;
+                        uint8_t* sf = ring + stage * C::kStageBytes + kATile + C::kBTile;
+#pragma unroll
+                        for (int i = 0; i < kRows; ++i)
+                            if (i < 2 || i0 + (i - 2) * 64 < NT)
+                                *reinterpret_cast<uint32_t*>(
+                                    sf + (i < 2 ? place(i0 + i * 64) : 512 + place(i0 + (i - 2) * 64))) =
+                                    cur[i][j];
+                        fence_proxy_async_smem();  // read by tcgen05.cp
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&aux->full[stage]);
+                        ++q;
+                    }
+#pragma unroll
+                    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) cur[i][j] = nxt[i][j];
+                }
             }
         }
-        cp_async_commit();
-        cp_async_wait<0>();  // no copy is still in flight when the CTA exits
     } else if (MODE == 0 && warp >= kGatherWarp0) {
         // ------------------------------------------------------------ gather (MODE 0)
         // Thread i copies the 16-byte chunks i, i + 128, ... of the tile's token rows (8 chunks a
@@ -457,13 +698,13 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         const uint8_t* src[C::kGIters];
         int q = 0, e = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < units && ok; u += gridDim.x) {
+        for (int u = unit0; u < units && ok; u += stride) {
             const Unit t = decode(u, e);
 #pragma unroll
             for (int i = 0; i < C::kGIters; ++i) {
-                const int j = (i0 + i * 128) >> 3;
+                const int j = first_token(t) + ((i0 + i * 128) >> 3);
                 src[i] = nullptr;
-                if (j < t.rows) {
+                if (j < t.rows && i0 + i * 128 < C::kBRows * 8) {
                     int r = g.rows[t.row + j];
                     if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
                     src[i] = g.a + (size_t)div_by(r, g.k, g.k_magic) * g.K + (i0 & 7) * 16;
@@ -497,7 +738,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
         const int lq = warp & 3;                     // TMEM lane quarter
         const int gt = (warp - kEpiWarp0 - grp * 4) * 32 + lane;
         int lu = 0, chunk = 0, e = 0;
-        for (int u = blockIdx.x; u < units; u += gridDim.x, ++lu) {
+        for (int u = unit0; u < units; u += stride, ++lu) {
             const Unit t = decode(u, e);
             const int b = lu % C::kNBuf;
             const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu / C::kNBuf) & 1), abort_flag);
@@ -512,7 +753,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                 // warp finishes the first 4, the up warp the others.  A warp's 32 lanes are
                 // then one MX block of act for each of its columns.
                 const bool up = lq >= 2;
-                const int feature = t.fb * 64 + (lq & 1) * 32;
+                const int feature = first_feature(t) + (lq & 1) * 32;
                 float* mine = reinterpret_cast<float*>(staging) + (warp - kEpiWarp0) * 512;
                 const float* other = reinterpret_cast<float*>(staging) + ((warp ^ 2) - kEpiWarp0) * 512;
                 for (int j0 = jbeg; j0 < jend; j0 += 8, ++chunk) {
@@ -551,7 +792,12 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&aux->tempty[b]);
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        arrive_leader(&aux->tempty[b]);
+                    else
+                        mbar_arrive(&aux->tempty[b]);
+                }
             } else {
                 // 1. drain this group's columns into registers as packed bf16 and hand them
                 //    back; 2. stage 8 token rows of 128 features at a time and store whole
@@ -573,9 +819,14 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&aux->tempty[b]);
+                if (lane == 0) {
+                    if constexpr (CG == 2)
+                        arrive_leader(&aux->tempty[b]);
+                    else
+                        mbar_arrive(&aux->tempty[b]);
+                }
                 const int jj = gt >> 4, cc = gt & 15;
-                const int col = t.fb * kBM + cc * 8;
+                const int col = first_feature(t) + cc * 8;
 #pragma unroll
                 for (int c = 0; c < C::kGroupCols; c += 8) {
                     if (jbeg + c < jend) {
@@ -603,10 +854,13 @@ __global__ void __launch_bounds__(Cfg<MODE, NT>::kThreads, 1)
     }
 
     tc_fence_before();
-    __syncthreads();
+    if constexpr (CG == 2)
+        cluster_sync();  // neither CTA leaves while the other may arrive on its barriers
+    else
+        __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc(tmem_base, C::kTmemCols);
+        tmem_release<CG>(tmem_base, C::kTmemCols);
     }
 }
 
@@ -629,19 +883,37 @@ cudaError_t tmap_e2m1(CUtensorMap* m, const void* base, uint64_t rows, uint64_t 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int MODE, int NT>
-cudaError_t launch_nt(const MxArgs& g, cudaStream_t st)
+template <int MODE, int NT, int CG = 1>
+cudaError_t launch_nt(MxArgs g, cudaStream_t st)
 {
-    using C = Cfg<MODE, NT>;
+    using C = Cfg<MODE, NT, CG>;
+    g.fb_count = (g.N + C::kFeatures - 1) / C::kFeatures;
+    auto magic = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (unsigned)d + 1) : 0u; };
+    g.fb_magic = magic(g.fb_count);
+    g.k_magic = magic(g.k);
     CUtensorMap tw, ta;
     cudaError_t e = tmap_e2m1(&tw, g.w, (uint64_t)g.E * g.N * (MODE == 0 ? 2 : 1), (uint64_t)g.K, 64);
     if (e == cudaSuccess)
-        e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, NT, kBK) : (ta = tw, e);
+        e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, C::kBRows, kBK)
+                      : (ta = tw, e);
     if (e != cudaSuccess) return e;
-    auto kern = mx_grouped_kernel<MODE, NT>;
+    auto kern = mx_grouped_kernel<MODE, NT, CG>;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(device_sms()), dim3(C::kThreads), C::kSmem, st, tw, ta, g);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(device_sms() / CG * CG);
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tw, ta, g);
 }
 
 template <int MODE>
@@ -650,7 +922,8 @@ cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
     if (most <= 16) return launch_nt<MODE, 16>(g, st);
     if (most <= 32) return launch_nt<MODE, 32>(g, st);
     if (most <= 64) return launch_nt<MODE, 64>(g, st);
-    return launch_nt<MODE, 128>(g, st);
+    if (g.R < 64 * g.E) return launch_nt<MODE, 128>(g, st);
+    return launch_nt<MODE, 224, 2>(g, st);
 }
 
 }  // namespace
@@ -662,14 +935,10 @@ cudaError_t launch_mx_grouped(const MxArgs& args, int mode, cudaStream_t st)
     const int most = mode == 2 ? g.R : g.R / g.k;
     g.early = mode == 1;
     g.stream_weights = most <= 64;
-    g.fb_count = mode == 0 ? g.N / 64 : (g.N + kBM - 1) / kBM;
-    auto magic = [](int d) { return d > 1 ? (uint32_t)((1ull << 32) / (unsigned)d + 1) : 0u; };
-    g.fb_magic = magic(g.fb_count);
     if (mode == 2) {
         g.rows = nullptr;
         g.k = 1;
     }
-    g.k_magic = magic(g.k);
     return mode == 0 ? launch_mode<0>(g, most, st) : launch_mode<1>(g, most, st);
 }
 
