@@ -14,8 +14,11 @@
 // costs at most 15 padded ones.  MODE 0's 128 weight rows are 64 gate rows and their
 // 64 up rows.
 //
-// Warp roles: 0 TMA (weights, MODE 1 also token rows); 1 TMEM and MMA issue; 2-3
-// scales; 4-11 epilogue; MODE 0: 12-15 gather of token rows.
+// Warp roles: 0 TMA; 1 TMEM and MMA issue; 2-3 scales; 4-11 epilogue; MODE 0: 12-15
+// gather of token rows.
+//   - Token rows: MODE 1 loads them by TMA with the weights; MODE 0 gathers x rows with
+//     16-byte cp.async copies straight to their swizzled places.  (26 gather4 TMA loads a
+//     stage, one per lane, issue too slowly: prefill's w13 took 1.70 ms instead of 0.97.)
 //   - Weights: TMA unpacks the 4-bit codes to the byte-wide slots that a mixed
 //     E2M1 x E4M3 MMA reads, so HBM and L2 move half a byte an element.
 //   - Scales: a K tile of 128 has 4 scale bytes per row.  They are copied 4 bytes at
@@ -152,6 +155,26 @@ __device__ __forceinline__ void tmem_release(uint32_t taddr, uint32_t cols)
                      : "memory");
 }
 
+// 16 TMEM lanes x 8 columns: lane i gets columns 2 (i % 4) and the next of TMEM lanes i / 4
+// (r[0], r[1]) and i / 4 + 8 (r[2], r[3]).
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+}
+
+// Four 8x8 matrices of 16-bit elements, transposed: lane i's register m holds rows 2 (i % 4)
+// and the next of column i / 4 of matrix m, and its address is that of row i % 8 of
+// matrix i / 8.
+__device__ __forceinline__ void store_matrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                      uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank()
 {
     uint32_t r;
@@ -167,11 +190,11 @@ __device__ __forceinline__ void cluster_sync()
 }
 
 // Arrive on the barrier that lies at this address in CTA 0 of the cluster.  It carries
-// only the fact.  What it stands for is a CTA's own shared memory, complete before the
-// arriving thread saw its own barrier (TMA tiles, and scales whose writers fenced the
-// async proxy), which the tensor core of that CTA's SM reads, or its own TMEM, read out
-// before tcgen05.wait::ld; so the default release (CTA scope) is enough.  A release at
-// cluster scope waits for the L2: 1200 cycles a stage, prefill 2.66 ms instead of 1.56.
+// only the fact.  What it stands for is in the arriving CTA: scales in its shared
+// memory, written and fenced towards the async proxy before, which the tensor core of
+// that CTA's own SM reads; or its TMEM, read out before tcgen05.wait::ld.  So the default
+// release (CTA scope) is enough.  A release at cluster scope waits for the L2: 1200
+// cycles a stage, prefill 2.66 ms instead of 1.56.
 __device__ __forceinline__ void arrive_leader(uint64_t* bar)
 {
     asm volatile(
@@ -179,6 +202,34 @@ __device__ __forceinline__ void arrive_leader(uint64_t* bar)
         "mapa.shared::cluster.u32 a, %0, 0;\n\t"
         "mbarrier.arrive.shared::cluster.b64 _, [a];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
+}
+
+// Address of the same shared-memory location in CTA 0 of the cluster.
+__device__ __forceinline__ uint32_t in_leader(const void* p)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+
+// 2D TMA load of a box at (c, row) into this CTA's shared memory whose bytes count on
+// `bar`.  CG = 2: `bar` may lie in the other CTA of the pair.
+template <int CG>
+__device__ __forceinline__ void tma_box(uint32_t dst, const void* tmap, uint32_t bar, int c, int row,
+                                        uint64_t policy)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
+            : "memory");
 }
 
 // mbar_wait for a barrier that the other CTA of the cluster arrives on.
@@ -237,18 +288,18 @@ __device__ __forceinline__ int div_by(int n, int d, uint32_t m)
 // NT: the most token rows of a tile (the MMA's N).
 template <int MODE, int NT, int CG>
 struct Cfg {
-    static constexpr int kThreads = MODE == 0 ? 512 : 384;
+    static constexpr int kThreads = 32 * (MODE == 0 ? kGatherWarp0 + kGatherWarps : kGatherWarp0);
     static constexpr int kBRows = NT / CG;                       // token rows in one CTA's B tile
     static constexpr int kBTile = kBRows * kBK;
     static constexpr int kSfbCols = 4 * ((NT + 127) / 128);      // TMEM columns of B's scales
     static constexpr int kSfCols = 4 + kSfbCols;
     static constexpr int kSfBytes = kSfCols * 128;
     static constexpr int kStageBytes = (kATile + kBTile + kSfBytes + 1023) & ~1023;
-    // epilogue staging: MODE 0: 8 warps x 2 x 8 columns x 32 lanes of fp32; MODE 1: 2
-    // groups x 2 x 8 token rows x 128 bf16
-    static constexpr int kStaging = MODE == 0 ? 16384 : 8192;
+    // epilogue: 8 warps x 2 buffers, MODE 0 of 4 columns x 32 lanes of fp32, MODE 1 of 8
+    // token rows x 32 bf16
+    static constexpr int kStaging = 8192;
     static constexpr int kTables = 2 * (kMaxExperts + 1) * 4 + 8 + 128;
-    static constexpr int kAux = 1024;
+    static constexpr int kAux = 512;
     static constexpr int kFixed = 1024 + kStaging + kTables + kAux;
     static constexpr int kNBuf = NT <= 64 ? 4 : 2;               // accumulators in flight
     static constexpr int kSfCol0 = kNBuf * NT;                   // first scale column
@@ -270,7 +321,6 @@ struct Cfg {
 struct Aux {
     uint64_t full[kMaxStages];
     uint64_t empty[kMaxStages];
-    uint64_t peer_full[kMaxStages];  // CG = 2: the second CTA's stage is full too
     uint64_t tfull[4];
     uint64_t tempty[4];
     uint64_t drain;
@@ -303,10 +353,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            // the producer's expect_tx, one arrival per scale warp and per gather warp
-            mbar_init(&aux->full[s], 1 + kScaleWarps + (MODE == 0 ? kGatherWarps : 0));
+            // the expect_tx, and one arrival per scale warp and per gather warp (CG = 2:
+            // CTA 0's barrier is the one that counts, for both CTAs)
+            mbar_init(&aux->full[s], 1 + CG * (kScaleWarps + (MODE == 0 ? kGatherWarps : 0)));
             mbar_init(&aux->empty[s], 1);
-            mbar_init(&aux->peer_full[s], 1);
         }
         for (int b = 0; b < C::kNBuf; ++b) {
             mbar_init(&aux->tfull[b], 1);
@@ -430,30 +480,35 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        const uint64_t pol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
+        const uint64_t wpol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
+        const uint64_t tpol = l2_policy_evict_last();  // token rows are read again per feature block
+        const uint32_t ring0 = smem_u32(ring);
         int stage = 0, fills = 0, e = 0;
         uint32_t phase = 0;
         bool ok = true, dep = !(MODE == 1 && g.early);
+        const uint32_t bytes = CG * (kATxBytes + (MODE == 1 ? C::kBTile : 0));
         for (int u = unit0; u < units && ok; u += stride) {
             const Unit t = decode(u, e);
-            const int row = weight_row(t);
+            const int row = weight_row(t), trow = t.row + first_token(t);
             for (int kt = 0; kt < num_kt; ++kt) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
                 if (!ok) break;
-                uint8_t* st = ring + stage * C::kStageBytes;
-                uint64_t* bar = &aux->full[stage];
+                const uint32_t st = ring0 + stage * C::kStageBytes;
+                const uint32_t bar = CG == 2 ? in_leader(&aux->full[stage]) : smem_u32(&aux->full[stage]);
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(bar, kATxBytes + (MODE == 1 ? C::kBTile : 0));
-                    tma_load_2d(st, &tm_w, bar, kt * kBK, row, pol);
-                    tma_load_2d(st + kATile / 2, &tm_w, bar, kt * kBK,
-                                row + (MODE == 0 ? g.N : kBM / 2), pol);
-                    if (MODE == 1) {
-                        if (!dep) pdl_wait();
-                        tma_load_2d_nohint(st + kATile, &tm_a, bar, kt * kBK, t.row + first_token(t));
+                    if (rank == 0) mbar_arrive_expect_tx(&aux->full[stage], bytes);
+                    tma_box<CG>(st, &tm_w, bar, kt * kBK, row, wpol);
+                    tma_box<CG>(st + kATile / 2, &tm_w, bar, kt * kBK, row + (MODE == 0 ? g.N : kBM / 2),
+                                wpol);
+                }
+                if (MODE == 1) {
+                    if (!dep) {
+                        pdl_wait();
+                        dep = true;
                     }
+                    if (elect_one()) tma_box<CG>(st + kATile, &tm_a, bar, kt * kBK, trow, tpol);
                 }
                 __syncwarp();
-                dep = true;
                 ++fills;
                 if (++stage == C::kStages) {
                     stage = 0;
@@ -464,8 +519,8 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
         if (!dep) pdl_wait();  // (no unit here) the grid still depends on it
         if (!ok || *abort_flag) {
             if (lane == 0) flag_error();
-            // let every TMA load already issued land before the CTA can exit
-            for (int s = 0; s < C::kStages; ++s) {
+            // let every TMA load already issued land before the CTA (CG = 2: the pair) can exit
+            for (int s = 0; s < C::kStages && rank == 0; ++s) {
                 const int n = fills > s ? (fills - s + C::kStages - 1) / C::kStages : 0;
                 if (n > 0) {
                     volatile int never = 0;
@@ -473,28 +528,8 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                 }
             }
         }
-    } else if (warp == 1 && CG == 2 && rank == 1) {
-        // ------------------------------------------------------------ relay (second CTA)
-        // CTA 0 issues the MMAs of both; tell it when a stage of this CTA is full.
-        int stage = 0;
-        uint32_t phase = 0;
-        bool ok = true;
-        for (int u = unit0; u < units && ok; u += stride) {
-            for (int kt = 0; kt < num_kt; ++kt) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&aux->full[stage], phase, abort_flag));
-                if (!ok) break;
-                if (elect_one()) {
-                    fence_proxy_async_smem();
-                    arrive_leader(&aux->peer_full[stage]);
-                }
-                __syncwarp();
-                if (++stage == C::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
-            }
-        }
-        if (!ok && lane == 0) flag_error();
+    } else if (warp == 1 && rank == 1) {
+        // the first CTA of the pair issues the MMAs of both
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         int stage = 0, lu = 0, e = 0;
@@ -512,9 +547,8 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
             const int n = padded(t.rows);
             const uint32_t d = tmem_base + (uint32_t)(b * NT), idesc = idesc_mx(CG * kBM, n);
             for (int kt = 0; kt < num_kt; ++kt) {
-                ok = __all_sync(0xffffffffu,
-                                mbar_wait(&aux->full[stage], phase, abort_flag) &&
-                                    (CG == 1 || mbar_wait_cluster(&aux->peer_full[stage], phase, abort_flag)));
+                ok = __all_sync(0xffffffffu, CG == 2 ? mbar_wait_cluster(&aux->full[stage], phase, abort_flag)
+                                                     : mbar_wait(&aux->full[stage], phase, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = ring0 + stage * C::kStageBytes;
@@ -523,7 +557,7 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                 const uint64_t da = umma_desc_sw128(sa), db = umma_desc_sw128(sb);
                 const uint64_t ds = scale_desc(sf);
                 if (elect_one()) {
-                    fence_proxy_async_smem();  // cp.async writes, read by the async proxy below
+                    if (CG == 1) fence_proxy_async_smem();  // scales and gathered rows came by cp.async
                     scales_to_tmem<CG>(tsf, ds);
 #pragma unroll
                     for (int i = 0; i < C::kSfbCols / 4; ++i)
@@ -586,21 +620,30 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
         if constexpr (CG == 1) {
             // Few token rows, many stages in flight: 4-byte cp.async copies, which arrive on the
             // stage's barrier when they land.
+            Unit t = {};
+            int tok[C::kSIters];
+            if (unit0 < units) {
+                t = decode(unit0, e);
+#pragma unroll
+                for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(t, i0 + i * 64);
+            }
             for (int u = unit0; u < units && ok; u += stride) {
-                const Unit t = decode(u, e);
+                const int rows = t.rows;
                 const uint8_t* src[kRows];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) src[i] = weight_src(t, i);
+                for (int i = 0; i < kRows; ++i) src[i] = i < 2 ? weight_src(t, i) : token_src(tok[i - 2]);
+                if (u + stride < units) {  // the next unit's rows are on their way during this one
+                    t = decode(u + stride, e);
 #pragma unroll
-                for (int i = 0; i < C::kSIters; ++i)
-                    src[2 + i] = i0 + i * 64 < t.rows ? token_src(token_row(t, i0 + i * 64)) : nullptr;
+                    for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(t, i0 + i * 64);
+                }
                 for (int kt = 0; kt < num_kt; ++kt, ++q) {
                     const int stage = q % C::kStages;
                     if (!wait_empty(stage)) break;
                     const uint32_t sf = smem_u32(ring + stage * C::kStageBytes + kATile + C::kBTile);
 #pragma unroll
                     for (int i = 0; i < kRows; ++i)
-                        if (i < 2 || src[i])
+                        if (i < 2 || i0 + (i - 2) * 64 < rows)
                             cp_async_4(sf + (i < 2 ? place(i0 + i * 64) : 512 + place(i0 + (i - 2) * 64)),
                                        src[i] + kt * 4);
                     cp_async_mbar_arrive(&aux->full[stage]);
@@ -611,9 +654,10 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
             cp_async_commit();
             cp_async_wait<0>();  // no copy is still in flight when the CTA exits
         } else {
-            // Many token rows: a 4-byte copy is one L1 line lookup a row and K tile, which
-            // competes with the gather.  So rows are read 4 K tiles at a time (16 bytes where
-            // the row pitch allows it), one group ahead, and stored from registers.
+            // Many token rows: a 4-byte copy is one L1 line lookup a row and K tile.  So rows are
+            // read a group of 4 K tiles at a time (16 bytes where the row pitch allows it), kAhead
+            // groups before they are stored from registers.
+            constexpr int kAhead = 2;
             const int align = (int)(ld & 15);  // 0: 16-byte rows, 8: 8-byte, else 4-byte
             auto load = [&](uint32_t (&w)[4], const uint8_t* p, int kt) {
                 p += kt * 4;
@@ -633,38 +677,47 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                         if (kt + j < num_kt) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
                 }
             };
-            uint32_t cur[kRows][4], nxt[kRows][4];
+            // The reader: the next group to load, and (one unit further) the rows of the unit after.
             const uint8_t* src[kRows];
-            int tok[C::kSIters];
-            Unit t = {};
-            if (unit0 < units) {
-                t = decode(unit0, e);
+            int tok[C::kSIters], ru = unit0, rkt = 0;
+            Unit rt = {};
+            auto next_rows = [&](int u) {
+                if (u >= units) return;
+                rt = decode(u, e);
 #pragma unroll
-                for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(t, i0 + i * 64);
+                for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(rt, i0 + i * 64);
+            };
+            auto read_group = [&](uint32_t (&w)[kRows][4]) {
+                if (ru >= units) return;
+                if (rkt == 0) {
 #pragma unroll
-                for (int i = 0; i < kRows; ++i) {
-                    src[i] = i < 2 ? weight_src(t, i) : token_src(tok[i - 2]);
-                    load(cur[i], src[i], 0);
+                    for (int i = 0; i < kRows; ++i) src[i] = i < 2 ? weight_src(rt, i) : token_src(tok[i - 2]);
+                    next_rows(ru + stride);
                 }
-            }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) load(w[i], src[i], rkt);
+                rkt += 4;
+                if (rkt >= num_kt) {
+                    rkt = 0;
+                    ru += stride;
+                }
+            };
+            uint32_t w[kAhead][kRows][4];
+            next_rows(unit0);
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) read_group(w[a]);
             for (int u = unit0; u < units && ok; u += stride) {
-                const bool more = u + stride < units;
-                if (more) {  // the next unit's rows, wanted at the end of this one
-                    t = decode(u + stride, e);
-#pragma unroll
-                    for (int i = 0; i < C::kSIters; ++i) tok[i] = token_row(t, i0 + i * 64);
-                }
                 for (int kt = 0; kt < num_kt && ok; kt += 4) {
-                    if (kt + 4 < num_kt) {
+                    uint32_t cur[kRows][4];
 #pragma unroll
-                        for (int i = 0; i < kRows; ++i) load(nxt[i], src[i], kt + 4);
-                    } else if (more) {
+                    for (int i = 0; i < kRows; ++i)
 #pragma unroll
-                        for (int i = 0; i < kRows; ++i) {
-                            src[i] = i < 2 ? weight_src(t, i) : token_src(tok[i - 2]);
-                            load(nxt[i], src[i], 0);
+                        for (int j = 0; j < 4; ++j) {
+                            cur[i][j] = w[0][i][j];
+#pragma unroll
+                            for (int a = 0; a + 1 < kAhead; ++a) w[a][i][j] = w[a + 1][i][j];
                         }
-                    }
+                    read_group(w[kAhead - 1]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (kt + j >= num_kt) break;
@@ -679,43 +732,58 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                                     cur[i][j];
                         fence_proxy_async_smem();  // read by tcgen05.cp
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&aux->full[stage]);
+                        if (lane == 0) arrive_leader(&aux->full[stage]);
                         ++q;
                     }
-#pragma unroll
-                    for (int i = 0; i < kRows; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) cur[i][j] = nxt[i][j];
                 }
             }
         }
     } else if (MODE == 0 && warp >= kGatherWarp0) {
         // ------------------------------------------------------------ gather (MODE 0)
-        // Thread i copies the 16-byte chunks i, i + 128, ... of the tile's token rows (8 chunks a
-        // row), straight to their swizzled places.
+        // Thread i copies the 16-byte chunks i, i + 128, ... of this CTA's token rows (8 chunks a
+        // row).  CG = 1: the copies arrive on the stage's barrier themselves.  CG = 2: that
+        // cannot reach the other CTA's barrier, so a warp waits for its copies of kLag stages
+        // ago, fences them towards the async proxy and arrives there.
+        constexpr int kLag = 3;
+        static_assert(kLag < C::kStages, "a stage is filled before its ring slot comes round");
         const int i0 = threadIdx.x - kGatherWarp0 * 32;
-        const uint64_t pol = l2_policy_evict_last();  // token rows are read again per block
-        const uint8_t* src[C::kGIters];
+        const uint64_t pol = l2_policy_evict_last();  // token rows are read again per feature block
         int q = 0, e = 0;
         bool ok = true;
-        for (int u = unit0; u < units && ok; u += stride) {
-            const Unit t = decode(u, e);
+        Unit t = {};
+        int r[C::kGIters];
+        auto next_rows = [&](int u) {
+            if (u >= units) return;
+            t = decode(u, e);
 #pragma unroll
             for (int i = 0; i < C::kGIters; ++i) {
-                const int j = first_token(t) + ((i0 + i * 128) >> 3);
-                src[i] = nullptr;
-                if (j < t.rows && i0 + i * 128 < C::kBRows * 8) {
-                    int r = g.rows[t.row + j];
-                    if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
-                    src[i] = g.a + (size_t)div_by(r, g.k, g.k_magic) * g.K + (i0 & 7) * 16;
+                const int j = (i0 + i * 128) >> 3;
+                r[i] = -1;
+                if (j < C::kBRows && first_token(t) + j < t.rows) {
+                    r[i] = g.rows[t.row + first_token(t) + j];
+                    if (!debug_in_range(r[i], 0, g.R, g.err)) r[i] = 0;
                 }
             }
+        };
+        auto arrive = [&](int stage) {  // CG = 2
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_leader(&aux->full[stage]);
+        };
+        next_rows(unit0);
+        for (int u = unit0; u < units && ok; u += stride) {
+            const uint8_t* src[C::kGIters];
+#pragma unroll
+            for (int i = 0; i < C::kGIters; ++i)
+                src[i] = r[i] < 0 ? nullptr
+                                  : g.a + (size_t)div_by(r[i], g.k, g.k_magic) * g.K + (i0 & 7) * 16;
+            next_rows(u + stride);  // on their way during this unit
             for (int kt = 0; kt < num_kt; ++kt, ++q) {
                 const int stage = q % C::kStages;
                 const uint32_t phase = (uint32_t)((q / C::kStages) & 1);
-                if (!__all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag))) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
+                if (!ok) {
                     if (lane == 0) flag_error();
-                    ok = false;
                     break;
                 }
                 const uint32_t sb = smem_u32(ring + stage * C::kStageBytes + kATile);
@@ -725,28 +793,59 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                     if (src[i])
                         cp_async_16_hint(sb + j * 128 + (((c & 7) ^ (j & 7)) << 4), src[i] + kt * kBK, pol);
                 }
-                cp_async_mbar_arrive(&aux->full[stage]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&aux->full[stage]);
+                if constexpr (CG == 1) {
+                    cp_async_mbar_arrive(&aux->full[stage]);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&aux->full[stage]);
+                } else {
+                    cp_async_commit();
+                    if (q >= kLag) {
+                        cp_async_wait<kLag>();
+                        arrive((q - kLag) % C::kStages);
+                    }
+                }
             }
         }
         cp_async_commit();
-        cp_async_wait<0>();
+        cp_async_wait<0>();  // no copy is still in flight when the CTA exits
+        if constexpr (CG == 2)
+            for (int p = max(q - kLag, 0); p < q && ok; ++p) arrive(p % C::kStages);
     } else {
         // ------------------------------------------------------------ epilogue
         const int grp = (warp - kEpiWarp0) >> 2;     // token-column group
         const int lq = warp & 3;                     // TMEM lane quarter
-        const int gt = (warp - kEpiWarp0 - grp * 4) * 32 + lane;
         int lu = 0, chunk = 0, e = 0;
+        auto release = [&](int b) {  // this warp has read accumulator b
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (CG == 2)
+                    arrive_leader(&aux->tempty[b]);
+                else
+                    mbar_arrive(&aux->tempty[b]);
+            }
+        };
         for (int u = unit0; u < units; u += stride, ++lu) {
             const Unit t = decode(u, e);
             const int b = lu % C::kNBuf;
+            const int jbeg = grp * C::kGroupCols, jend = min(t.rows, jbeg + C::kGroupCols);
+            // MODE 1: lane i holds the y rows of the group's columns i, i + 32, ...
+            int yrow[(C::kGroupCols + 31) / 32] = {};
+            if (MODE == 1) {
+#pragma unroll
+                for (int i = 0; i < (C::kGroupCols + 31) / 32; ++i) {
+                    const int j = jbeg + i * 32 + lane;
+                    if (j < jend) {
+                        yrow[i] = g.rows ? g.rows[t.row + j] : t.row + j;
+                        if (!debug_in_range(yrow[i], 0, g.R, g.err)) yrow[i] = 0;
+                    }
+                }
+            }
             const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu / C::kNBuf) & 1), abort_flag);
             if (!got) flag_error();
             if (named_bar_or(1 + grp, 128, !got || *abort_flag)) break;  // same in all 4 warps
             tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * NT);
-            const int jbeg = grp * C::kGroupCols, jend = min(t.rows, jbeg + C::kGroupCols);
             if constexpr (MODE == 0) {
                 // Lanes 0-63 hold gate rows, 64-127 the up rows of the same features.  Warps lq
                 // and lq ^ 2 exchange 4 of every 8 columns through shared memory: the gate
@@ -754,13 +853,13 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                 // then one MX block of act for each of its columns.
                 const bool up = lq >= 2;
                 const int feature = first_feature(t) + (lq & 1) * 32;
-                float* mine = reinterpret_cast<float*>(staging) + (warp - kEpiWarp0) * 512;
-                const float* other = reinterpret_cast<float*>(staging) + ((warp ^ 2) - kEpiWarp0) * 512;
+                float* mine = reinterpret_cast<float*>(staging) + (warp - kEpiWarp0) * 256;
+                const float* other = reinterpret_cast<float*>(staging) + ((warp ^ 2) - kEpiWarp0) * 256;
                 for (int j0 = jbeg; j0 < jend; j0 += 8, ++chunk) {
                     uint32_t v[8];
                     tmem_ld8(acc + j0, v);
                     tmem_ld_wait();
-                    const int buf = (chunk & 1) * 256;
+                    const int buf = (chunk & 1) * 128;
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         mine[buf + i * 32 + lane] = __uint_as_float(up ? v[i] : v[4 + i]);
@@ -790,65 +889,55 @@ __global__ void __launch_bounds__(Cfg<MODE, NT, CG>::kThreads, 1)
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2)
-                        arrive_leader(&aux->tempty[b]);
-                    else
-                        mbar_arrive(&aux->tempty[b]);
-                }
+                release(b);
             } else {
-                // 1. drain this group's columns into registers as packed bf16 and hand them
-                //    back; 2. stage 8 token rows of 128 features at a time and store whole
-                //    row segments.  Two buffers, one barrier per chunk.
+                // Drain this group's columns into registers as packed bf16 and hand them back,
+                // then transpose 8 token rows of this warp's 32 features at a time through
+                // its own 512 bytes of shared memory and store 16 bytes a lane.  The 16x256b
+                // load gives a lane two tokens of feature lane / 4, which is the fragment that
+                // a transposing stmatrix takes; 16-byte chunk c of row r lies at c ^ (r / 2), so
+                // neither its 8 rows nor the reads share a bank.  No barrier but the warp's.
                 uint32_t pk[C::kGroupCols / 2];
+                constexpr int kBatch = 4;  // column blocks per wait
 #pragma unroll
-                for (int c = 0; c < C::kGroupCols; c += 8) {
-                    if (jbeg + c < jend) {
-                        uint32_t v[8];
-                        tmem_ld8(acc + jbeg + c, v);
-                        tmem_ld_wait();
+                for (int c0 = 0; c0 < C::kGroupCols / 8; c0 += kBatch) {
+                    uint32_t v[kBatch][8];
 #pragma unroll
-                        for (int i = 0; i < 8; i += 2) {
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[i]),
-                                                                           __uint_as_float(v[i + 1]));
-                            pk[(c + i) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                    for (int c = c0; c < c0 + kBatch && c < C::kGroupCols / 8; ++c)
+                        if (jbeg + c * 8 < jend) {
+                            tmem_ld_16x256(acc + jbeg + c * 8, v[c - c0]);
+                            tmem_ld_16x256(acc + (16u << 16) + jbeg + c * 8, v[c - c0] + 4);
                         }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = c0; c < c0 + kBatch && c < C::kGroupCols / 8; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(
+                                __uint_as_float(v[c - c0][2 * i]), __uint_as_float(v[c - c0][2 * i + 1]));
+                            pk[c * 4 + i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                }
+                release(b);
+                const int f = first_feature(t) + lq * 32 + (lane & 3) * 8;
+                __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(g.y) + f;
+                uint8_t* const mine = staging + (warp - kEpiWarp0) * 1024;
+                const uint32_t put = smem_u32(mine) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
+                const uint8_t* const get = mine + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) << 4);
+#pragma unroll
+                for (int c = 0; c < C::kGroupCols / 8; ++c) {
+                    if (jbeg + c * 8 < jend) {
+                        const int buf = (c & 1) * 512;
+                        store_matrix_x4_trans(put + buf, pk[c * 4], pk[c * 4 + 1], pk[c * 4 + 2], pk[c * 4 + 3]);
+                        __syncwarp();
+                        const uint4 val = *reinterpret_cast<const uint4*>(get + buf);
+                        const int j = c * 8 + (lane >> 2);
+                        const int row = __shfl_sync(0xffffffffu, yrow[c / 4], j & 31);
+                        if (jbeg + j < jend && f < g.N)
+                            *reinterpret_cast<uint4*>(y + (size_t)row * g.N) = val;
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if constexpr (CG == 2)
-                        arrive_leader(&aux->tempty[b]);
-                    else
-                        mbar_arrive(&aux->tempty[b]);
-                }
-                const int jj = gt >> 4, cc = gt & 15;
-                const int col = first_feature(t) + cc * 8;
-#pragma unroll
-                for (int c = 0; c < C::kGroupCols; c += 8) {
-                    if (jbeg + c < jend) {
-                        uint8_t* buf = staging + (grp * 2 + (chunk & 1)) * 2048;
-#pragma unroll
-                        for (int r = 0; r < 8; ++r) {
-                            const uint32_t w = pk[(c + r) / 2];
-                            reinterpret_cast<uint16_t*>(buf + r * 256)[lq * 32 + lane] =
-                                (uint16_t)((r & 1) ? (w >> 16) : (w & 0xFFFFu));
-                        }
-                        named_bar_sync(1 + grp, 128);
-                        if (jbeg + c + jj < jend && col < g.N) {
-                            const int p = t.row + jbeg + c + jj;
-                            const uint4 val = *reinterpret_cast<const uint4*>(buf + jj * 256 + cc * 16);
-                            const int row = g.rows ? g.rows[p] : p;
-                            if (debug_in_range(row, 0, g.R, g.err))
-                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(g.y) +
-                                                          (size_t)row * g.N + col) = val;
-                        }
-                        ++chunk;
-                    }
-                }
+                __syncwarp();  // the buffers are free again
             }
         }
     }
@@ -923,7 +1012,7 @@ cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
     if (most <= 32) return launch_nt<MODE, 32>(g, st);
     if (most <= 64) return launch_nt<MODE, 64>(g, st);
     if (g.R < 64 * g.E) return launch_nt<MODE, 128>(g, st);
-    return launch_nt<MODE, 224, 2>(g, st);
+    return launch_nt<MODE, 208, 2>(g, st);
 }
 
 }  // namespace
