@@ -1,0 +1,405 @@
+// mx_gemm.cuh -- pieces shared by the two kernels of the microscaled grouped products
+// (mx_pair.cu: many rows per expert; mx_stream.cu: few): block-scaled MMA wrappers, the
+// tiles of the groups, and the scale loaders.
+//
+//   D[m, n] = sum_b 2^(sa[m, b] + sb[n, b] - 254) sum_{i in block b} a[m, i] b[n, i]
+//
+// with E2M1 weights and E4M3 tokens (one of them a, the other b), blocks of 32 and E8M0
+// scales.  Products of codes and their power-of-two scales are exact, so only the fp32
+// sums round.
+//
+// Weights lie in shared memory one byte an element: TMA unpacks the 4-bit codes to the
+// slots that a mixed E2M1 x E4M3 MMA reads, so HBM and L2 move half a byte an element.
+//
+// A K tile of 128 has 4 scale bytes per row.  They are laid out as tcgen05.cp spreads them
+// over tensor memory (row r of 128 at byte 16 (r % 32) + 4 (r / 32) of 512).  Every ring
+// stage has its own scale columns in tensor memory, so a stage's copy never has to wait for
+// another stage's MMAs.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "gemm_common.cuh"
+#include "kernels.h"
+#include "mx_common.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace mx {
+
+constexpr int kBK = 128;                    // K elements per stage: one 128-byte swizzle row
+constexpr int kMaxExperts = 1024;
+// weight rows of one TMA box (MODE 0 loads gate and up rows of 32 features in turn)
+template <int MODE>
+constexpr int kWBox = MODE == 0 ? 32 : 64;
+constexpr int kRowTx = kBK / 2;             // an unpacking TMA load counts its packed bytes
+constexpr int kScaleStages = 5;             // the fewest ring stages that run_scale_team allows
+constexpr int kSfCols = 16;                 // TMEM columns per stage for scales: 4 + 8 used
+constexpr int kTableBytes = 2 * (kMaxExperts + 1) * 4 + 120;
+
+// ------------------------------------------------------------------ PTX
+
+// One lane of a converged warp, the same one every time.  The loops of the TMA and
+// MMA warps run in all 32 lanes and only the issue is the elected lane's: the
+// descriptors then stay in uniform registers, which the tensor instructions take
+// their operands from (a loop inside `if (lane == 0)` took 60 cycles to issue one MMA).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// The outcome of a wait that every lane of a warp polled for itself, agreed on by all.  The
+// lanes may leave their polling loops at different times, and neither the loop nor the vote
+// promises that the warp runs converged afterwards, which elect.sync and the .aligned
+// tensor instructions after it need: hence the __syncwarp.
+__device__ __forceinline__ bool warp_agrees(bool ok)
+{
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();
+    return ok;
+}
+
+// Instruction descriptor of kind::mxf8f6f4, both operands K-major, E8M0 scales.  Format
+// codes: E4M3 0, E2M1 5.
+__host__ __device__ constexpr uint32_t idesc_formats(bool a_is_weight)
+{
+    return (a_is_weight ? 5u << 7 : 5u << 10) | (1u << 23);
+}
+__device__ __forceinline__ uint32_t idesc_shape(int M, int N)
+{
+    return ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+// Its bits that select the scale byte of K block kb, 0..3, for B and A.
+__device__ __forceinline__ constexpr uint32_t idesc_kb(int kb)
+{
+    return ((uint32_t)kb << 4) | ((uint32_t)kb << 29);
+}
+
+// CG: CTAs that work on one MMA (cta_group::1 or ::2).
+template <int CG>
+__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                     uint32_t sfb, uint32_t accumulate)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+            "[%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// Shared-memory descriptor of 512 bytes of scales: 32 rows of 16 bytes, no swizzle,
+// groups of 8 rows 128 bytes apart.
+__device__ __forceinline__ uint64_t scale_desc(uint32_t smem)
+{
+    return (uint64_t)((smem >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) |
+           ((uint64_t)1 << 46);
+}
+
+// Copies them to 4 TMEM columns, the same 32 lanes' worth in every lane quarter.
+// Ordered before later MMAs of this thread.  With CG = 2 each of the two CTAs copies from
+// its own shared memory to its own TMEM.
+template <int CG>
+__device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc)
+{
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+                     : "memory");
+}
+
+// 2D TMA load of a box at (c, row) into this CTA's shared memory whose bytes count on
+// `bar`.  CG = 2: `bar` may lie in the other CTA of the pair.
+template <int CG>
+__device__ __forceinline__ void tma_2d(uint32_t dst, const void* tmap, uint32_t bar, int c, int row,
+                                       uint64_t policy)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
+            : "memory");
+}
+
+// ------------------------------------------------------------------ groups and tiles
+
+// n / d for 0 <= n < 2^31 by a multiplication with m = floor(2^32 / d) + 1 (d = 1: m = 0).
+// The product can be one too large where n d is large; that is put right.
+__device__ __forceinline__ int div_by(int n, int d, uint32_t m)
+{
+    int q = d == 1 ? n : (int)__umulhi((uint32_t)n, m);
+    if (q * d > n) --q;
+    return q;
+}
+
+// A tile: `rows` token rows from `row`, the feature block `fb` of `expert`.
+struct Unit {
+    int expert, fb, row, rows;
+};
+
+// The groups of a call, derived from expert_offsets by every CTA itself, so that there is no
+// tile list and no launch for one.
+struct Groups {
+    const int* first;  // [E + 1] tiles before each expert
+    const int* start;  // [E + 1] rows before each expert
+    int E;
+
+    // Unit u of tiles x fbs: experts in order; within one, feature block major and tile
+    // minor, so the tiles that share a weight block run at the same time on neighbouring
+    // CTAs and share it in L2.  A group of c rows in t tiles is cut evenly (to 16 rows).
+    // All 32 lanes take part; `e` is the expert of this warp's unit before (a CTA's units
+    // ascend, so the search starts there, 32 experts at a time).
+    __device__ __forceinline__ Unit unit(int u, int fbs, uint32_t fb_magic, int& e) const
+    {
+        const int lane = threadIdx.x & 31;
+        const int rest = div_by(u, fbs, fb_magic);
+        for (;;) {  // to the last e with first[e] <= rest
+            const int at = e + 1 + lane;
+            const uint32_t past = __ballot_sync(0xffffffffu, at > E || first[min(at, E)] > rest);
+            if (past) {
+                e += __ffs(past) - 1;
+                break;
+            }
+            e += 32;
+        }
+        const int local = u - first[e] * fbs, count = first[e + 1] - first[e];
+        const int rows = start[e + 1] - start[e];
+        Unit t;
+        t.expert = e;
+        t.fb = local;
+        t.row = start[e];
+        t.rows = rows;
+        if (count > 1) {
+            const int per = ((rows + count - 1) / count + 15) & ~15;
+            t.fb = local / count;
+            const int at = (local - t.fb * count) * per;
+            t.row += at;
+            t.rows = min(per, rows - at);
+        }
+        return t;
+    }
+};
+
+// Fills first / start (kTableBytes of shared memory at `tables`) for tiles of up to nt rows.
+// Offsets are clamped to 0 .. R and to ascending order, so that none leads outside the
+// operands.  All kThreads threads call it; it ends with a barrier.
+template <int kThreads>
+__device__ __forceinline__ Groups build_groups(const MxArgs& g, int nt, int* tables)
+{
+    int* first = tables;
+    int* start = tables + kMaxExperts + 1;
+    int* warp_sum = start + kMaxExperts + 1;
+    constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+    static_assert(kThreads / 32 * 4 <= 120, "warp_sum");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int tiles[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        tiles[i] = 0;
+        if (e < g.E) {
+            const int a = min(max(__ldcg(g.offsets + e), 0), g.R);
+            const int b = min(max(__ldcg(g.offsets + e + 1), a), g.R);
+            start[e] = a;
+            if (e == g.E - 1) start[g.E] = b;
+            tiles[i] = (b - a + nt - 1) / nt;
+        }
+        sum += tiles[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x * kPer + i;
+        if (e < g.E) first[e] = before;
+        before += tiles[i];
+        if (e == g.E - 1) first[g.E] = before;
+    }
+    __syncthreads();
+    return Groups{first, start, g.E};
+}
+
+// ------------------------------------------------------------------ scales
+
+// Byte of row r's 4 scales in a K tile's layout.
+__device__ __forceinline__ uint32_t scale_place(int r)
+{
+    return (uint32_t)((r >> 7) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4);
+}
+
+// Feature of row r of a MODE 0 tile, without the feature block's part, and whether the row is its
+// up row: 32 gate rows, their 32 up rows, and so on.
+__device__ __forceinline__ int tile_feature(int r) { return r / 64 * 32 + r % 32; }
+__device__ __forceinline__ bool tile_row_is_up(int r) { return r / 32 % 2; }
+
+// One team of 64 threads that brings scales into the ring.  Reading 4 bytes a row and K tile
+// costs one L1 line lookup each, so a row is read a group of 4 K tiles at a time (16 bytes
+// where the row pitch allows it) into registers, one of the team's groups ahead, and stored
+// 4 bytes a stage.  A stage costs a team about 600 cycles (stores, the fence towards
+// tcgen05.cp's proxy, the arrival, the loads), so two teams take the groups in turn.  A team
+// steps over the other's group of 4 stages, and a wait on a ring slot must not be two
+// rounds ahead of the slot: that takes more than 4 stages (kScaleStages).
+//   kRows       rows of this thread; put[i]: where row i's bytes go within a stage's scales,
+//               or -1
+//   sources(u, src)  sets the rows' first scale bytes for unit u
+//   wait(q)     waits until ring fill q may be written (false: give up)
+//   stage(q)    shared memory of that fill's scales
+//   arrive(q)   called by every lane after its warp's stores are fenced
+template <int kRows, typename Sources, typename Wait, typename Stage, typename Arrive>
+__device__ __forceinline__ void run_scale_team(int team, int unit0, int stride, int units, int num_kt,
+                                               int row_bytes, const int (&put)[kRows], Sources sources,
+                                               Wait wait, Stage stage, Arrive arrive)
+{
+    const int align = row_bytes & 15;  // 0: 16-byte rows, 8: 8-byte, else 4-byte
+    const int groups = (num_kt + 3) / 4;
+    const uint8_t* src[kRows];
+    // the reader's place: unit, group in the unit, the unit that src belongs to
+    int ru = unit0, rg = team, have = -1;
+    auto settle = [&] {
+        while (rg >= groups && ru < units) {
+            rg -= groups;
+            ru += stride;
+        }
+    };
+    auto read = [&](uint32_t (&w)[kRows][4]) {
+        if (ru >= units) return;
+        if (have != ru) {
+            sources(ru, src);
+            have = ru;
+        }
+        const int kt = rg * 4;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const uint8_t* p = src[i] + kt * 4;
+            if (align == 0) {
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+                w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+            } else if (align == 8) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+                w[i][0] = v.x, w[i][1] = v.y;
+                if (kt + 2 < num_kt) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p) + 1);
+                    w[i][2] = x.x, w[i][3] = x.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (kt + j < num_kt) w[i][j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+            }
+        }
+        rg += 2;
+        settle();
+    };
+    uint32_t next[kRows][4];
+    settle();
+    int u = ru, grp = rg, lu = (ru - unit0) / stride;  // the writer's place
+    read(next);
+    while (u < units) {
+        uint32_t cur[kRows][4];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) cur[i][j] = next[i][j];
+        read(next);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (grp * 4 + j >= num_kt) break;
+            const int q = lu * num_kt + grp * 4 + j;
+            if (!wait(q)) return;
+            uint8_t* const sf = stage(q);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                if (put[i] >= 0) *reinterpret_cast<uint32_t*>(sf + put[i]) = cur[i][j];
+            fence_proxy_async_smem();
+            __syncwarp();
+            arrive(q);
+        }
+        grp += 2;
+        while (grp >= groups) {
+            grp -= groups;
+            u += stride;
+            ++lu;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+inline uint32_t magic(int d) { return d > 1 ? (uint32_t)((1ull << 32) / (unsigned)d + 1) : 0u; }
+
+// E2M1 codes [rows, cols / 2]: boxes of box_rows x 128 elements, unpacked to one byte slot an
+// element with the 128-byte swizzle.
+inline cudaError_t weights_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols,
+                               uint32_t box_rows)
+{
+    gemm::EncodeTiledFn fn = gemm::get_encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols / 2};
+    const cuuint32_t box[2] = {(cuuint32_t)kBK, box_rows};
+    const cuuint32_t ones[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(base), dims,
+                          strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <typename Kern>
+cudaError_t launch(Kern kern, int grid, int cluster, int threads, int smem, cudaStream_t st,
+                   const CUtensorMap& tw, const CUtensorMap& ta, const MxArgs& g)
+{
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, tw, ta, g);
+}
+
+}  // namespace mx
+}  // namespace moe

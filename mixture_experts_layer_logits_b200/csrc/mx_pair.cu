@@ -1,0 +1,651 @@
+// mx_pair.cu -- microscaled grouped products for many token rows per expert: two CTAs of a
+// cluster work on one MMA (cta_group::2, M = 256 weight rows, N up to 208 token rows).
+//
+//   MODE 0  act[p, f] = MX(silu(gate) * up) of x[rows[p] / k] with w13[e] rows f and I + f
+//   MODE 1  y[rows[p] or p, f] = w[e] row f dotted with act (or any E4M3 rows) [p]
+//
+// Weights are the M operand and an expert's token rows the N columns, rounded up to 16 per
+// tile, so a ragged group costs at most 15 padded columns.  A pair of CTAs reads each weight
+// row and each token row once (its half of both per CTA): the single-CTA form with N = 128 was
+// bound by L2 (11.5 TB/s of operand reads) at 2.11 ms for T = 8192, E = 128, k = 8, H = 4096,
+// I = 1536.
+//
+// Warp roles: 0 TMA; 1 TMEM, and in CTA 0 MMA issue for both; 2-3 and 12-13 scales (two
+// teams); 4-11 epilogue; MODE 0: 14-15 gather of token rows.
+//   - MODE 1 loads token rows by TMA with the weights; MODE 0 gathers x rows with 16-byte
+//     cp.async copies straight to their swizzled places.  (26 gather4 TMA loads a stage, one
+//     per lane, issue too slowly: w13 took 1.70 ms instead of 0.97.)
+//   - Both CTAs' loads count on CTA 0's full barriers; the commit of a stage's MMAs frees it
+//     in both.
+// Every mbarrier wait is bounded; on a timeout the kernel records the error word, stops
+// issuing, drains what it issued and frees TMEM.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mx_gemm.cuh"
+
+namespace moe {
+
+namespace {
+
+using namespace mx;
+using gemm::named_bar_or;
+using gemm::named_bar_sync;
+using gemm::silu_mul;
+
+constexpr int kBM = 128;                  // weight rows of one CTA's tile
+constexpr int kATile = kBM * kBK;
+constexpr int kNT = 208;                  // the most token rows of a tile
+constexpr int kBRows = kNT / 2;           // token rows in one CTA's B tile
+constexpr int kBTile = kBRows * kBK;
+constexpr int kSfBytes = 512 + 1024;      // scales of the weight rows and of all token rows
+constexpr int kStageBytes = (kATile + kBTile + kSfBytes + 1023) & ~1023;
+constexpr int kStages = 6;
+static_assert(kStages >= kScaleStages, "ring");
+constexpr int kTmemCols = 512;            // 2 accumulators of 208 columns, 6 x 16 of scales
+constexpr int kSfCol0 = 2 * kNT;
+static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "TMEM");
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kScaleWarpB = 12, kGatherWarp0 = 14, kGatherWarps = 2;
+constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);  // whole warpgroups; MODE 1 leaves two warps idle
+constexpr int kGroupCols = kNT / 2;       // token columns per epilogue group of four warps
+// epilogue shared memory per warp: MODE 0, 2 buffers of 8 columns x 32 lanes of fp32 to swap, and 2
+// of 8 token rows of 32 E4M3 codes (48 bytes apart: the rows that a store hits share no bank);
+// MODE 1, 2 buffers of 8 token rows x 32 bf16
+constexpr int kCodePitch = 48;
+constexpr int kWarpStaging = 2 * 1024 + 2 * 8 * kCodePitch;
+
+template <int MODE>
+struct Cfg {
+    static constexpr int kStaging = kEpiWarps * (MODE == 0 ? kWarpStaging : 1024);
+    static constexpr int kSmem = 1024 + kStages * kStageBytes + kStaging + 512 + kTableBytes;
+    static constexpr int kFeatures = MODE == 0 ? 64 : 128;   // output features of one CTA
+    static constexpr int kGIters = (kBRows * 8 + kGatherWarps * 32 - 1) / (kGatherWarps * 32);
+    static_assert(kSmem <= 232448, "shared memory");
+};
+
+struct Aux {
+    uint64_t full[kStages];
+    uint64_t empty[kStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+};
+
+// Arrive on the barrier at this address in both CTAs when every tensor instruction issued so
+// far by this thread is done.
+__device__ __forceinline__ void commit(uint64_t* bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile(
+        "barrier.cluster.arrive.release;\n\t"
+        "barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Address of the same shared-memory location in CTA 0 of the cluster.
+__device__ __forceinline__ uint32_t in_leader(const void* p)
+{
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+    return a;
+}
+
+// Arrive on the barrier that lies at this address in CTA 0 of the cluster.  It carries
+// only the fact.  What it stands for is in the arriving CTA: scales and gathered rows in its
+// shared memory, written and fenced towards the async proxy before, which the tensor core
+// of that CTA's own SM reads; or its TMEM, read out before tcgen05.wait::ld.  So the default
+// release (CTA scope) is enough.  A release at cluster scope waits for the L2: 1200 cycles
+// a stage, prefill 2.66 ms instead of 1.52.
+__device__ __forceinline__ void arrive_leader(uint64_t* bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_leader(bar)) : "memory");
+}
+
+// mbar_wait for a barrier that the other CTA of the cluster arrives on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort)
+{
+    uint64_t t0 = 0;
+    for (uint32_t n = 1;; ++n) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((n & 255u) == 0) {
+            if (*abort) return false;
+            const uint64_t t = globaltimer_ns();
+            if (!t0) t0 = t;
+            if (t - t0 > 2000000000ull) return false;
+        }
+    }
+}
+
+// 16 TMEM lanes x 8 columns: lane i gets columns 2 (i % 4) and the next of TMEM lanes i / 4
+// (r[0], r[1]) and i / 4 + 8 (r[2], r[3]).
+__device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t* r)
+{
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(taddr));
+}
+
+// Four 8x8 matrices of 16-bit elements, transposed: lane i's register m holds rows 2 (i % 4)
+// and the next of column i / 4 of matrix m, and its address is that of row i % 8 of
+// matrix i / 8.
+__device__ __forceinline__ void store_matrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                                      uint32_t d)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+                 "r"(a), "r"(b), "r"(c), "r"(d)
+                 : "memory");
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+                   const MxArgs g)
+{
+    using C = Cfg<MODE>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    uint8_t* staging = ring + kStages * kStageBytes;
+    Aux* aux = reinterpret_cast<Aux*>(staging + C::kStaging);
+    static_assert(sizeof(Aux) <= 512, "aux area");
+
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            // CTA 0's counts: the expect_tx, and from both CTAs one arrival per warp of a scale
+            // team and per gather warp
+            mbar_init(&aux->full[s], 1 + 2 * (2 + (MODE == 0 ? kGatherWarps : 0)));
+            mbar_init(&aux->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&aux->tfull[b], 1);
+            mbar_init(&aux->tempty[b], 2 * kEpiWarps);
+        }
+        mbar_init(&aux->drain, 1);
+        aux->abort = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tm_w);
+        if (MODE == 1) tma_prefetch_desc(&tm_a);
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(&aux->tmem_base)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    // The second product of the FFN (g.early) takes only act from the launch before it;
+    // expert_offsets, rows and weights were complete before that launch passed its own
+    // wait, so the tables and the first weight tiles need not wait for it.
+    if (!g.early) pdl_wait();
+    pdl_launch_dependents();
+    const Groups groups =
+        build_groups<kThreads>(g, kNT, reinterpret_cast<int*>(staging + C::kStaging + 512));
+    tc_fence_before();
+    cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
+    tc_fence_after();
+
+    uint32_t rank;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    const int unit0 = (int)blockIdx.x / 2, stride = (int)gridDim.x / 2;
+    const uint32_t tmem_base = aux->tmem_base;
+    volatile int* abort_flag = &aux->abort;
+    auto flag_error = [&] {
+        atomicExch(g.err, kDeviceErrorMagic);
+        aux->abort = 1;
+    };
+    const int fbs = g.fb_count[0];
+    const int units = groups.first[g.E] * fbs;
+    const int num_kt = g.K / kBK;
+    auto unit = [&](int u, int& e) { return groups.unit(u, fbs, g.fb_magic[0], e); };
+    auto padded = [](int rows) { return (rows + 15) & ~15; };  // the MMA's N
+    // this CTA's part of a unit: its first output feature, and its first token row in the tile.
+    // MODE 1: the second CTA's features may begin past N; it then works on the first ones
+    // again, and stores none of them.
+    auto first_feature = [&](const Unit& t) { return (t.fb * 2 + (int)rank) * C::kFeatures; };
+    auto first_token = [&](const Unit& t) { return (int)rank * (padded(t.rows) / 2); };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ TMA producer
+        const uint64_t wpol = l2_policy_evict_normal();
+        const uint64_t tpol = l2_policy_evict_last();  // token rows are read again per feature block
+        const uint32_t ring0 = smem_u32(ring);
+        const uint32_t bytes = 2 * (kBM * kRowTx + (MODE == 1 ? kBTile : 0));
+        int stage = 0, fills = 0, e = 0;
+        uint32_t phase = 0;
+        bool ok = true, dep = !(MODE == 1 && g.early);
+        for (int u = unit0; u < units && ok; u += stride) {
+            const Unit t = unit(u, e);
+            const int f = first_feature(t);
+            const int row = MODE == 0 ? t.expert * 2 * g.N + f : t.expert * g.N + (f < g.N ? f : 0);
+            const int trow = t.row + first_token(t);
+            for (int kt = 0; kt < num_kt; ++kt) {
+                ok = warp_agrees(mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
+                if (!ok) break;
+                const uint32_t st = ring0 + stage * kStageBytes;
+                const uint32_t bar = in_leader(&aux->full[stage]);
+                if (elect_one()) {
+                    if (rank == 0) mbar_arrive_expect_tx(&aux->full[stage], bytes);
+#pragma unroll
+                    for (int r = 0; r < kBM; r += kWBox<MODE>)
+                        tma_2d<2>(st + r * kBK, &tm_w, bar, kt * kBK,
+                                  row + (MODE == 0 ? tile_feature(r) + (tile_row_is_up(r) ? g.N : 0) : r), wpol);
+                }
+                if (MODE == 1) {
+                    if (!dep) {
+                        pdl_wait();
+                        dep = true;
+                    }
+                    __syncwarp();
+                    if (elect_one()) tma_2d<2>(st + kATile, &tm_a, bar, kt * kBK, trow, tpol);
+                }
+                __syncwarp();
+                ++fills;
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!dep) pdl_wait();  // (no unit here) the grid still depends on it
+        if (!ok || *abort_flag) {
+            if (lane == 0) flag_error();
+            // let every TMA load already issued land before the pair can exit
+            for (int s = 0; s < kStages && rank == 0; ++s) {
+                const int n = fills > s ? (fills - s + kStages - 1) / kStages : 0;
+                if (n > 0) {
+                    volatile int never = 0;
+                    mbar_wait(&aux->full[s], (uint32_t)((n - 1) & 1), &never, 500000000ull);
+                }
+            }
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ------------------------------------------------------------ MMA issuer
+        int stage = 0, lu = 0, e = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const uint32_t ring0 = smem_u32(ring);
+        for (int u = unit0; u < units && ok; u += stride, ++lu) {
+            const Unit t = unit(u, e);
+            const int b = lu & 1;
+            ok = warp_agrees(mbar_wait_cluster(&aux->tempty[b], (uint32_t)((lu >> 1) & 1) ^ 1u, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const int n = padded(t.rows);
+            const uint32_t d = tmem_base + (uint32_t)(b * kNT);
+            const uint32_t idesc = idesc_formats(true) | idesc_shape(2 * kBM, n);
+            for (int kt = 0; kt < num_kt; ++kt) {
+                ok = warp_agrees(mbar_wait_cluster(&aux->full[stage], phase, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sa = ring0 + stage * kStageBytes;
+                const uint32_t sb = sa + kATile, sf = sb + kBTile;
+                const uint32_t tsf = tmem_base + (uint32_t)(kSfCol0 + stage * kSfCols);
+                const uint64_t da = umma_desc_sw128(sa), db = umma_desc_sw128(sb);
+                const uint64_t ds = scale_desc(sf);
+                if (elect_one()) {
+                    scales_to_tmem<2>(tsf, ds);
+                    scales_to_tmem<2>(tsf + 4, ds + (512 >> 4));
+                    if (n > 128) scales_to_tmem<2>(tsf + 8, ds + (1024 >> 4));
+#pragma unroll
+                    for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along K
+                        umma<2>(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
+                                (kt | kk) ? 1u : 0u);
+                    commit(&aux->empty[stage]);
+                    if (kt + 1 == num_kt) commit(&aux->tfull[b]);
+                }
+                __syncwarp();
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok && lane == 0) flag_error();
+        __syncwarp();
+        // all MMAs and copies issued by this warp are complete before TMEM is freed
+        if (elect_one()) commit(&aux->drain);
+        __syncwarp();
+        volatile int never = 0;
+        if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
+    } else if (warp == 2 || warp == 3 || warp == kScaleWarpB || warp == kScaleWarpB + 1) {
+        // ------------------------------------------------------------ scales
+        // Thread i of a team handles weight rows i and i + 64 of this CTA's tile and token rows
+        // i, i + 64, ... of the whole tile (each CTA needs them all).
+        const int team = warp >= kScaleWarpB;
+        const int i0 = (team ? warp - kScaleWarpB : warp - 2) * 32 + lane;
+        const size_t ld = (size_t)g.K / 32;
+        if (MODE == 1 && g.early) pdl_wait();  // act's scales
+        constexpr int kRows = 2 + 4;
+        int put[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = i0 + (i < 2 ? i : i - 2) * 64;
+            put[i] = i < 2 ? (int)scale_place(r) : r < kNT ? (int)(512 + scale_place(r)) : -1;
+        }
+        int e = 0;
+        auto sources = [&](int u, const uint8_t* (&src)[kRows]) {
+            const Unit t = unit(u, e);
+            const int f = first_feature(t);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // MODE 1: rows past N belong to features that are never stored
+                const int r = i0 + i * 64;
+                const int row = MODE == 0 ? t.expert * 2 * g.N + f + tile_feature(r) +
+                                                (tile_row_is_up(r) ? g.N : 0)
+                                          : t.expert * g.N + min(f + r, g.N - 1);
+                src[i] = g.w_scale + (size_t)row * ld;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // past the tile's end any scale will do
+                int r = t.row + min(i0 + i * 64, t.rows - 1);
+                if (MODE == 0) {
+                    r = g.rows[r];
+                    if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
+                    r = div_by(r, g.k, g.k_magic);
+                }
+                src[2 + i] = g.a_scale + (size_t)r * ld;
+            }
+        };
+        run_scale_team<kRows>(
+            team, unit0, stride, units, num_kt, (int)ld, put, sources,
+            [&](int q) {
+                const bool ok = warp_agrees(mbar_wait(&aux->empty[q % kStages],
+                                                                  (uint32_t)((q / kStages) & 1) ^ 1u,
+                                                                  abort_flag));
+                if (!ok && lane == 0) flag_error();
+                return ok;
+            },
+            [&](int q) { return ring + (q % kStages) * kStageBytes + kATile + kBTile; },
+            [&](int q) {
+                if (lane == 0) arrive_leader(&aux->full[q % kStages]);
+            });
+    } else if (MODE == 0 && warp >= kGatherWarp0) {
+        // ------------------------------------------------------------ gather (MODE 0)
+        // Thread i copies the 16-byte chunks i, i + 64, ... of this CTA's token rows (8 chunks a
+        // row).  The copies cannot arrive on the other CTA's barrier themselves, so a warp
+        // waits for its copies of kLag stages ago, fences them towards the async proxy and
+        // arrives there.
+        constexpr int kLag = 3;
+        static_assert(kLag < kStages, "a stage is filled before its ring slot comes round");
+        const int i0 = threadIdx.x - kGatherWarp0 * 32;
+        const uint64_t pol = l2_policy_evict_last();
+        int q = 0, e = 0;
+        bool ok = true;
+        int r[C::kGIters];
+        auto next_rows = [&](int u) {
+            if (u >= units) return;
+            const Unit t = unit(u, e);
+#pragma unroll
+            for (int i = 0; i < C::kGIters; ++i) {
+                const int j = (i0 + i * kGatherWarps * 32) >> 3;
+                r[i] = -1;
+                if (j < kBRows && first_token(t) + j < t.rows) {
+                    r[i] = g.rows[t.row + first_token(t) + j];
+                    if (!debug_in_range(r[i], 0, g.R, g.err)) r[i] = 0;
+                }
+            }
+        };
+        auto arrive = [&](int stage) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_leader(&aux->full[stage]);
+        };
+        next_rows(unit0);
+        for (int u = unit0; u < units && ok; u += stride) {
+            const uint8_t* src[C::kGIters];
+#pragma unroll
+            for (int i = 0; i < C::kGIters; ++i)
+                src[i] = r[i] < 0 ? nullptr
+                                  : g.a + (size_t)div_by(r[i], g.k, g.k_magic) * g.K + (i0 & 7) * 16;
+            next_rows(u + stride);  // on their way during this unit
+            for (int kt = 0; kt < num_kt; ++kt, ++q) {
+                const int stage = q % kStages;
+                const uint32_t phase = (uint32_t)((q / kStages) & 1);
+                ok = warp_agrees(mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
+                if (!ok) {
+                    if (lane == 0) flag_error();
+                    break;
+                }
+                const uint32_t sb = smem_u32(ring + stage * kStageBytes + kATile);
+#pragma unroll
+                for (int i = 0; i < C::kGIters; ++i) {
+                    const int c = i0 + i * kGatherWarps * 32, j = c >> 3;
+                    if (src[i])
+                        cp_async_16_hint(sb + j * 128 + (((c & 7) ^ (j & 7)) << 4), src[i] + kt * kBK, pol);
+                }
+                cp_async_commit();
+                if (q >= kLag) {
+                    cp_async_wait<kLag>();
+                    arrive((q - kLag) % kStages);
+                }
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();  // no copy is still in flight when the CTA exits
+        for (int p = max(q - kLag, 0); p < q && ok; ++p) arrive(p % kStages);
+    } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
+        // ------------------------------------------------------------ epilogue
+        const int grp = (warp - kEpiWarp0) >> 2;     // token-column group
+        const int lq = warp & 3;                     // TMEM lane quarter
+        const int jbeg = grp * kGroupCols;
+        constexpr int kBlocks = kGroupCols / 8;      // column blocks of 8
+        auto release = [&](int b) {  // this warp has read accumulator b
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_leader(&aux->tempty[b]);
+        };
+        int lu = 0, e = 0;
+        for (int u = unit0; u < units; u += stride, ++lu) {
+            const Unit t = unit(u, e);
+            const int b = lu & 1;
+            const int jend = min(t.rows, jbeg + kGroupCols);
+            // MODE 1: lane i holds the y rows of the group's columns i, i + 32, ...
+            int yrow[(kGroupCols + 31) / 32] = {};
+            if (MODE == 1) {
+#pragma unroll
+                for (int i = 0; i < (kGroupCols + 31) / 32; ++i) {
+                    const int j = jbeg + i * 32 + lane;
+                    if (j < jend) {
+                        yrow[i] = g.rows ? g.rows[t.row + j] : t.row + j;
+                        if (!debug_in_range(yrow[i], 0, g.R, g.err)) yrow[i] = 0;
+                    }
+                }
+            }
+            const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu >> 1) & 1), abort_flag);
+            if (!got) flag_error();
+            // same in all 4 warps; also: the group is done with the unit before's staging
+            if (named_bar_or(1 + grp, 128, !got || *abort_flag)) break;
+            __syncwarp();
+            tc_fence_after();
+            const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * kNT);
+            if constexpr (MODE == 0) {
+                // Warps 0 and 2 of a group hold the gates of 32 features, an MX block of act, and
+                // warps 1 and 3 their ups.  Of every two column blocks the gate warp finishes the
+                // first and the up warp the second: they swap the other halves through shared
+                // memory.  A lane then has features lane / 4 + 0, 8, 16, 24 of tokens 2 (lane % 4)
+                // and the next; codes leave as 32-byte rows.
+                const int up = lq & 1;
+                uint8_t* const ex = staging + (warp - kEpiWarp0) * kWarpStaging;
+                const uint8_t* const other = staging + ((warp ^ 1) - kEpiWarp0) * kWarpStaging;
+                uint8_t* const codes = ex + 2 * 1024;
+                const int f = first_feature(t) + (lq >> 1) * 32;
+                int step = 0;
+                for (int c = 0; c < kBlocks && jbeg + c * 8 < jend; c += 2, ++step) {
+                    const bool two = c + 1 < kBlocks;
+                    uint32_t v[2][8];
+                    tmem_ld_16x256(acc + jbeg + c * 8, v[0]);
+                    tmem_ld_16x256(acc + (16u << 16) + jbeg + c * 8, v[0] + 4);
+                    if (two) {
+                        tmem_ld_16x256(acc + jbeg + c * 8 + 8, v[1]);
+                        tmem_ld_16x256(acc + (16u << 16) + jbeg + c * 8 + 8, v[1] + 4);
+                    }
+                    tmem_ld_wait();
+                    const int buf = (step & 1) * 1024;
+                    uint32_t own[8], give[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        own[i] = up ? v[1][i] : v[0][i];
+                        give[i] = up ? v[0][i] : v[1][i];
+                    }
+                    reinterpret_cast<uint4*>(ex + buf)[lane] = make_uint4(give[0], give[1], give[2], give[3]);
+                    reinterpret_cast<uint4*>(ex + buf)[32 + lane] = make_uint4(give[4], give[5], give[6], give[7]);
+                    named_bar_sync(3 + grp * 2 + (lq >> 1), 64);
+                    const uint4 o0 = reinterpret_cast<const uint4*>(other + buf)[lane];
+                    const uint4 o1 = reinterpret_cast<const uint4*>(other + buf)[32 + lane];
+                    const uint32_t got8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+                    const int cb = c + up;  // the block that this warp finishes
+                    if (cb >= kBlocks || jbeg + cb * 8 >= jend) continue;  // warp-uniform
+                    float a[8];  // even: the first token
+                    uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float x = __uint_as_float(own[i]), z = __uint_as_float(got8[i]);
+                        a[i] = up ? silu_mul(z, x) : silu_mul(x, z);
+                        const uint32_t bits = __float_as_uint(a[i]) & 0x7FFFFFFFu;
+                        if (i & 1)
+                            m1 = max(m1, bits);
+                        else
+                            m0 = max(m0, bits);
+                    }
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) {
+                        m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
+                        m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                    }
+                    const uint32_t s0 = scale_code(m0, kEmaxE4M3), s1 = scale_code(m1, kEmaxE4M3);
+                    const float i0 = inverse_scale(min(s0, 254u)), i1 = inverse_scale(min(s1, 254u));
+                    uint32_t q0 = e4m3x4(a[0] * i0, a[2] * i0, a[4] * i0, a[6] * i0);
+                    uint32_t q1 = e4m3x4(a[1] * i1, a[3] * i1, a[5] * i1, a[7] * i1);
+                    if (s0 == kNanScale) q0 = 0x7F7F7F7Fu;
+                    if (s1 == kNanScale) q1 = 0x7F7F7F7Fu;
+                    // 8 tokens x 32 codes, rows kCodePitch apart
+                    uint8_t* const put = codes + (step & 1) * (8 * kCodePitch) + (lane & 3) * (2 * kCodePitch) + (lane >> 2);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        put[i * 8] = (uint8_t)(q0 >> (8 * i));
+                        put[kCodePitch + i * 8] = (uint8_t)(q1 >> (8 * i));
+                    }
+                    __syncwarp();
+                    const int p = t.row + jbeg + cb * 8;
+                    if (lane < 16 && jbeg + cb * 8 + (lane >> 1) < jend)
+                        *reinterpret_cast<uint4*>(g.act + (size_t)(p + (lane >> 1)) * g.N + f + (lane & 1) * 16) =
+                            *reinterpret_cast<const uint4*>(codes + (step & 1) * (8 * kCodePitch) +
+                                                            (lane >> 1) * kCodePitch + (lane & 1) * 16);
+                    // lanes 0 .. 3 hold the scales of tokens 2 lane and 2 lane + 1
+                    if (lane < 4) {
+                        uint8_t* const sc = g.act_scale + (size_t)(p + lane * 2) * (g.N / 32) + f / 32;
+                        if (jbeg + cb * 8 + lane * 2 < jend) sc[0] = (uint8_t)s0;
+                        if (jbeg + cb * 8 + lane * 2 + 1 < jend) sc[g.N / 32] = (uint8_t)s1;
+                    }
+                    __syncwarp();
+                }
+                release(b);
+            } else {
+                // Drain this group's columns into registers as packed bf16 and hand them back,
+                // then transpose 8 token rows of this warp's 32 features at a time through
+                // its own 512 bytes of shared memory and store 16 bytes a lane.  The 16x256b
+                // load gives a lane two tokens of feature lane / 4, which is the fragment that
+                // a transposing stmatrix takes; 16-byte chunk c of row r lies at c ^ (r / 2), so
+                // neither its 8 rows nor the reads share a bank.  No barrier but the warp's.
+                uint32_t pk[kBlocks * 4];
+                constexpr int kBatch = 4;  // column blocks per wait
+#pragma unroll
+                for (int c0 = 0; c0 < kBlocks; c0 += kBatch) {
+                    uint32_t v[kBatch][8];
+#pragma unroll
+                    for (int c = c0; c < c0 + kBatch && c < kBlocks; ++c)
+                        if (jbeg + c * 8 < jend) {
+                            tmem_ld_16x256(acc + jbeg + c * 8, v[c - c0]);
+                            tmem_ld_16x256(acc + (16u << 16) + jbeg + c * 8, v[c - c0] + 4);
+                        }
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = c0; c < c0 + kBatch && c < kBlocks; ++c)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(
+                                __uint_as_float(v[c - c0][2 * i]), __uint_as_float(v[c - c0][2 * i + 1]));
+                            pk[c * 4 + i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                }
+                release(b);
+                const int f = first_feature(t) + lq * 32 + (lane & 3) * 8;
+                __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(g.y) + f;
+                uint8_t* const mine = staging + (warp - kEpiWarp0) * 1024;
+                const uint32_t put = smem_u32(mine) + (lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4);
+                const uint8_t* const get = mine + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 3)) << 4);
+#pragma unroll
+                for (int c = 0; c < kBlocks; ++c) {
+                    if (jbeg + c * 8 < jend) {
+                        const int buf = (c & 1) * 512;
+                        store_matrix_x4_trans(put + buf, pk[c * 4], pk[c * 4 + 1], pk[c * 4 + 2], pk[c * 4 + 3]);
+                        __syncwarp();
+                        const uint4 val = *reinterpret_cast<const uint4*>(get + buf);
+                        const int j = c * 8 + (lane >> 2);
+                        const int row = __shfl_sync(0xffffffffu, yrow[c / 4], j & 31);
+                        if (jbeg + j < jend && f < g.N)
+                            *reinterpret_cast<uint4*>(y + (size_t)row * g.N) = val;
+                    }
+                }
+                __syncwarp();  // the buffers are free again
+            }
+        }
+    }
+
+    tc_fence_before();
+    cluster_sync();  // neither CTA leaves while the other may arrive on its barriers
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
+                     "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+template <int MODE>
+cudaError_t launch_mode(MxArgs g, cudaStream_t st)
+{
+    using C = Cfg<MODE>;
+    g.fb_count[0] = (g.N + 2 * C::kFeatures - 1) / (2 * C::kFeatures);
+    g.fb_magic[0] = magic(g.fb_count[0]);
+    CUtensorMap tw, ta;
+    cudaError_t e = weights_map(&tw, g.w, (uint64_t)g.E * g.N * (MODE == 0 ? 2 : 1), (uint64_t)g.K,
+                                kWBox<MODE>);
+    if (e == cudaSuccess)
+        e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, kBRows, kBK)
+                      : (ta = tw, e);
+    if (e != cudaSuccess) return e;
+    return launch(mx_pair_kernel<MODE>, device_sms() / 2 * 2, 2, kThreads, C::kSmem, st, tw, ta, g);
+}
+
+}  // namespace
+
+cudaError_t launch_mx_pair(const MxArgs& g, int mode, cudaStream_t st)
+{
+    return mode == 0 ? launch_mode<0>(g, st) : launch_mode<1>(g, st);
+}
+
+}  // namespace moe
