@@ -11,6 +11,7 @@ torch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -327,11 +328,23 @@ def _same(t: torch.Tensor, name: str, dtype, shape, device):
     return t.data_ptr()
 
 
-def _out(t, name, dtype, shape, device):
-    """The given output tensor, checked, or a new one."""
+# A call of one of these on a few rows takes the host longer than the GPU, so the checks and
+# allocations below are the cheapest forms that torch has.
+
+
+def _out(t, name, like, dtype, shape):
+    """The given output tensor, checked, or a new one on the device of `like`."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _same(t, name, dtype, torch.Size(shape), device)
+        return like.new_empty(shape, dtype=dtype)
+    _same(t, name, dtype, torch.Size(shape), like.device)
+    return t
+
+
+def _out_like(t, name, like, dtype):
+    """_out of the shape of `like`."""
+    if t is None:
+        return torch.empty_like(like) if dtype is like.dtype else torch.empty_like(like, dtype=dtype)
+    _same(t, name, dtype, like.shape, like.device)
     return t
 
 
@@ -340,12 +353,11 @@ def _call(fn, where, device, *args):
     if device.type != "cuda":
         raise ValueError(f"{where}: expected CUDA tensors, got {device}")
     index = device.index
-    stream = torch.cuda.current_stream(index).cuda_stream
     if index == torch.cuda.current_device():
-        status = fn(*args, stream)
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, stream)
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if status != MOE_OK:
         raise MoeError(status, where)
 
@@ -364,8 +376,8 @@ def moe_quantize_mx(src: torch.Tensor, fmt: str = "e2m1", codes=None, scales=Non
     if cols < 32 or cols % 32 or src.numel() == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_quantize_mx")
     dev = src.device
-    codes = _out(codes, "codes", torch.uint8, (*lead, cols // 2 if fmt == "e2m1" else cols), dev)
-    scales = _out(scales, "scales", torch.uint8, (*lead, cols // 32), dev)
+    codes = _out(codes, "codes", src, torch.uint8, (*lead, cols // 2 if fmt == "e2m1" else cols))
+    scales = _out(scales, "scales", src, torch.uint8, (*lead, cols // 32))
     _call(load_library().moe_quantize_mx, "moe_quantize_mx", dev, src.data_ptr(),
           _MX_SOURCES[src.dtype], src.numel() // cols, cols, _MX_FORMATS[fmt], codes.data_ptr(),
           scales.data_ptr())
@@ -391,14 +403,14 @@ def moe_add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool 
     pr = ps = pc = psc = None
     if residual is not None:
         pr = _same(residual, "residual", bf16, shape, dev)
-        sum_out = _out(sum_out, "sum_out", bf16, shape, dev)
+        sum_out = _out_like(sum_out, "sum_out", x, bf16)
         ps = sum_out.data_ptr()
     elif sum_out is not None:
         raise ValueError("sum_out: there is no residual to add")
-    out = _out(out, "out", bf16, shape, dev)
+    out = _out_like(out, "out", x, bf16)
     if quantize:
-        codes = _out(codes, "codes", torch.uint8, shape, dev)
-        scales = _out(scales, "scales", torch.uint8, (T, H // 32), dev)
+        codes = _out_like(codes, "codes", x, torch.uint8)
+        scales = _out(scales, "scales", x, torch.uint8, (T, H // 32))
         pc, psc = codes.data_ptr(), scales.data_ptr()
     elif codes is not None or scales is not None:
         raise ValueError("codes, scales: given without quantize=True")
@@ -407,8 +419,15 @@ def moe_add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool 
     return sum_out, out, codes, scales
 
 
+@functools.lru_cache(maxsize=4096)
+def _mm_plan(R, E, N, K):
+    """(MmShape, workspace bytes)."""
+    shape = MmShape(R, E, N, K)
+    return shape, int(load_library().moe_grouped_mm_workspace_size(shape))
+
+
 def moe_grouped_mm_workspace_size(R: int, E: int, N: int, K: int) -> int:
-    return int(load_library().moe_grouped_mm_workspace_size(MmShape(R, E, N, K)))
+    return _mm_plan(R, E, N, K)[1]
 
 
 def moe_grouped_mm_mx4(a, a_scale, w, w_scale, expert_offsets, ws=None, y=None):
@@ -422,7 +441,7 @@ def moe_grouped_mm_mx4(a, a_scale, w, w_scale, expert_offsets, ws=None, y=None):
     R, K = a.shape
     E, N, _ = w.shape
     dev, u8, size = a.device, torch.uint8, torch.Size
-    need = moe_grouped_mm_workspace_size(R, E, N, K)
+    shape, need = _mm_plan(R, E, N, K)
     if need == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_grouped_mm_mx4")
     ptrs = (_same(a, "a", u8, size((R, K)), dev),
@@ -430,15 +449,22 @@ def moe_grouped_mm_mx4(a, a_scale, w, w_scale, expert_offsets, ws=None, y=None):
             _same(w, "w", u8, size((E, N, K // 2)), dev),
             _same(w_scale, "w_scale", u8, size((E, N, K // 32)), dev),
             _same(expert_offsets, "expert_offsets", torch.int32, size((E + 1,)), dev))
-    y = _out(y, "y", torch.bfloat16, (R, N), dev)
-    ws = _workspace_of(ws, need, dev)
-    _call(load_library().moe_grouped_mm_mx4, "moe_grouped_mm_mx4", dev, *ptrs,
-          MmShape(R, E, N, K), y.data_ptr(), ws.data_ptr(), ws.numel())
+    y = _out(y, "y", a, torch.bfloat16, (R, N))
+    ws = _workspace_of(ws, need, a)
+    _call(load_library().moe_grouped_mm_mx4, "moe_grouped_mm_mx4", dev, *ptrs, shape,
+          y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
 
 
+@functools.lru_cache(maxsize=4096)
+def _mx4_plan(T, E, top_k, H, I):
+    """(Shape, workspace bytes)."""
+    shape = Shape(T, E, top_k, H, I)
+    return shape, int(load_library().moe_mx4_workspace_size(shape))
+
+
 def moe_mx4_workspace_size(T: int, E: int, top_k: int, H: int, I: int) -> int:
-    return int(load_library().moe_mx4_workspace_size(Shape(T, E, top_k, H, I)))
+    return _mx4_plan(T, E, top_k, H, I)[1]
 
 
 def workspace_mx4(T: int, E: int, top_k: int, H: int, I: int, device="cuda") -> torch.Tensor:
@@ -449,11 +475,12 @@ def workspace_mx4(T: int, E: int, top_k: int, H: int, I: int, device="cuda") -> 
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _workspace_of(ws, need, device):
+def _workspace_of(ws, need, like):
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if ws.dtype is not torch.uint8 or ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws: expected contiguous uint8 on {device}, got {ws.dtype} on {ws.device}")
+        return like.new_empty(need, dtype=torch.uint8)
+    if ws.dtype is not torch.uint8 or ws.device != like.device or not ws.is_contiguous():
+        raise ValueError(f"ws: expected contiguous uint8 on {like.device}, got {ws.dtype} on "
+                         f"{ws.device}")
     return ws
 
 
@@ -464,8 +491,7 @@ def _mx4_operands(where, x, x_scale, w13, w13_scale, w2, w2_scale, top_k):
     T, H = x.shape
     E = w13.shape[0]
     I = w13.shape[1] // 2
-    shape = Shape(T, E, top_k, H, I)
-    need = int(load_library().moe_mx4_workspace_size(shape))
+    shape, need = _mx4_plan(T, E, top_k, H, I)
     if need == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, where)
     dev, u8, size = x.device, torch.uint8, torch.Size
@@ -488,8 +514,8 @@ def moe_grouped_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, expert_offsets
     dev, R = x.device, shape.T * top_k
     off = _same(expert_offsets, "expert_offsets", torch.int32, torch.Size((shape.E + 1,)), dev)
     rows = _same(permuted_rows, "permuted_rows", torch.int32, torch.Size((R,)), dev)
-    y = _out(y, "y", torch.bfloat16, (R, shape.H), dev)
-    ws = _workspace_of(ws, need, dev)
+    y = _out(y, "y", x, torch.bfloat16, (R, shape.H))
+    ws = _workspace_of(ws, need, x)
     _call(load_library().moe_grouped_ffn_mx4, "moe_grouped_ffn_mx4", dev, *ptrs, off, rows, shape,
           y.data_ptr(), ws.data_ptr(), ws.numel())
     return y
@@ -509,8 +535,8 @@ def moe_forward_mx4(x, x_scale, logits, w13, w13_scale, w2, w2_scale, top_k: int
                                       (topk_weights, "topk_weights", torch.float32, (T, top_k)),
                                       (expert_offsets, "expert_offsets", torch.int32, (E + 1,)),
                                       (permuted_rows, "permuted_rows", torch.int32, (T * top_k,)))]
-    out = _out(out, "out", torch.bfloat16, (T, shape.H), dev)
-    ws = _workspace_of(ws, need, dev)
+    out = _out(out, "out", x, torch.bfloat16, (T, shape.H))
+    ws = _workspace_of(ws, need, x)
     _call(load_library().moe_forward_mx4, "moe_forward_mx4", dev, *ptrs[:2], plog, *ptrs[2:],
           shape, out.data_ptr(), *extra, ws.data_ptr(), ws.numel())
     return out

@@ -21,6 +21,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "gemm_common.cuh"
 #include "kernels.h"
 #include "mx_common.cuh"
@@ -379,12 +381,21 @@ inline cudaError_t weights_map(CUtensorMap* m, const void* base, uint64_t rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <typename Kern>
-cudaError_t launch(Kern kern, int grid, int cluster, int threads, int smem, cudaStream_t st,
+template <auto kern>
+cudaError_t launch(int grid, int cluster, int threads, int smem, cudaStream_t st,
                    const CUtensorMap& tw, const CUtensorMap& ta, const MxArgs& g)
 {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    // the attribute stays with the kernel (one `done` per instantiation), so it is set once a device
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (!(done.load(std::memory_order_relaxed) & bit) || !bit) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(bit, std::memory_order_relaxed);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(threads);

@@ -638,7 +638,7 @@ cudaError_t launch_mode(MxArgs g, cudaStream_t st)
         e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, kBRows, kBK)
                       : (ta = tw, e);
     if (e != cudaSuccess) return e;
-    return launch(mx_pair_kernel<MODE>, device_sms() / 2 * 2, 2, kThreads, C::kSmem, st, tw, ta, g);
+    return launch<mx_pair_kernel<MODE>>(device_sms() / 2 * 2, 2, kThreads, C::kSmem, st, tw, ta, g);
 }
 
 }  // namespace

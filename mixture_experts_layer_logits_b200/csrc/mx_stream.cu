@@ -495,7 +495,7 @@ cudaError_t launch_nt(MxArgs g, cudaStream_t st)
     if (e == cudaSuccess)
         e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, NT, kBK) : (ta = tw, e);
     if (e != cudaSuccess) return e;
-    return launch(mx_stream_kernel<MODE, NT>, device_sms(), 1, kThreads, C::kSmem, st, tw, ta, g);
+    return launch<mx_stream_kernel<MODE, NT>>(device_sms(), 1, kThreads, C::kSmem, st, tw, ta, g);
 }
 
 template <int MODE>
