@@ -243,8 +243,13 @@ __device__ __forceinline__ Groups build_groups(const MxArgs& g, int nt, int* tab
     }
     if (lane == 31) warp_sum[warp] = incl;
     __syncthreads();
-    int before = incl - sum;
-    for (int w = 0; w < warp; ++w) before += warp_sum[w];
+    int ws = lane < kThreads / 32 ? warp_sum[lane] : 0, wincl = ws;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, wincl, o);
+        if (lane >= o) wincl += v;
+    }
+    int before = incl - sum + __shfl_sync(0xffffffffu, wincl - ws, warp);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x * kPer + i;

@@ -36,35 +36,42 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
 // ------------------------------------------------------------------ quantisation
 
 // A matrix whose columns are a multiple of 32 is a run of blocks, whatever its rows:
-// four consecutive threads hold one block, 8 elements each.
-template <bool E2M1, typename Src>
+// four consecutive threads hold one block, 8 elements each.  HBM-bound; a thread has U
+// chunks' loads in flight before it uses the first (201 M bf16 elements to E2M1: U = 1
+// 104 us, 2 86 us, 4 78.5 us, which is the measured copy rate, 8 80 us).
+template <bool E2M1, typename Src, int U>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const Src* __restrict__ src, long chunks, uint8_t* __restrict__ codes,
                     uint8_t* __restrict__ scales)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const long c = (long)blockIdx.x * blockDim.x + threadIdx.x;  // 8-element chunk
-    const bool live = c < chunks;
-    float v[8] = {};
-    if (live) {
+    const long c0 = (long)blockIdx.x * (256 * U) + threadIdx.x;  // 8-element chunks c0 + 256 u
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long c = min(c0 + 256 * u, chunks - 1);
         if constexpr (sizeof(Src) == 2) {
-            unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(src) + c), v);
+            unpack_bf16x8(__ldcs(reinterpret_cast<const uint4*>(src) + c), v[u]);
         } else {
             const float4 a = __ldcs(reinterpret_cast<const float4*>(src) + 2 * c);
             const float4 b = __ldcs(reinterpret_cast<const float4*>(src) + 2 * c + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-            v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+            v[u][0] = a.x, v[u][1] = a.y, v[u][2] = a.z, v[u][3] = a.w;
+            v[u][4] = b.x, v[u][5] = b.y, v[u][6] = b.z, v[u][7] = b.w;
         }
     }
-    uint2 q;
-    const uint32_t s = mx::quantize8<E2M1>(v, q);
-    if (!live) return;
-    if constexpr (E2M1)
-        reinterpret_cast<uint32_t*>(codes)[c] = q.x;
-    else
-        reinterpret_cast<uint2*>(codes)[c] = q;
-    if ((c & 3) == 0) scales[c >> 2] = (uint8_t)s;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const long c = c0 + 256 * u;
+        uint2 q;
+        const uint32_t s = mx::quantize8<E2M1>(v[u], q);
+        if (c >= chunks) continue;
+        if constexpr (E2M1)
+            reinterpret_cast<uint32_t*>(codes)[c] = q.x;
+        else
+            reinterpret_cast<uint2*>(codes)[c] = q;
+        if ((c & 3) == 0) scales[c >> 2] = (uint8_t)s;
+    }
 }
 
 // ------------------------------------------------------------------ norm
@@ -151,27 +158,46 @@ cudaError_t launch_norm(const NormArgs& a, int threads, cudaStream_t st)
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st)
 {
     const int chunks = a.H / 8;
-    const int c = (chunks + 1023) / 1024;  // 8-element chunks per thread
-    const int threads = ((chunks + c - 1) / c + 31) & ~31;
-    if (c <= 1) return launch_norm<1>(a, threads, st);
-    if (c <= 2) return launch_norm<2>(a, threads, st);
-    if (c <= 4) return launch_norm<4>(a, threads, st);
-    return launch_norm<8>(a, threads, st);
+    // Chunks of 8 elements: one per thread where there are few rows, and CTAs of 256 threads
+    // where rows fill the SMs (8192 x 4096 with residual and blocks: 48.5 us, 97% of the measured
+    // copy rate; with CTAs of 512 54.6 us, of 128 53.1 us).
+    const int most = a.T >= 4 * device_sms() ? 256 : 1024;
+    const int c = (chunks + most - 1) / most;
+    const int cc = c <= 1 ? 1 : c <= 2 ? 2 : c <= 4 ? 4 : 8;
+    const int threads = ((chunks + cc - 1) / cc + 31) & ~31;
+    if (cc == 1) return launch_norm<1>(a, threads, st);
+    if (cc == 2) return launch_norm<2>(a, threads, st);
+    if (cc == 4) return launch_norm<4>(a, threads, st);
+    return launch_norm<8>(a, threads > 1024 ? 1024 : threads, st);
+}
+
+template <bool E2M1, typename Src, int U>
+static cudaError_t launch_quantize(const void* src, long chunks, uint8_t* codes, uint8_t* scales,
+                                   cudaStream_t st)
+{
+    return launch_pdl(quantize_kernel<E2M1, Src, U>, dim3((unsigned)((chunks + 256 * U - 1) / (256 * U))),
+                      dim3(256), 0, st, static_cast<const Src*>(src), chunks, codes, scales);
+}
+
+template <typename Src, int U>
+static cudaError_t launch_quantize(const void* src, long chunks, bool e2m1, uint8_t* codes,
+                                   uint8_t* scales, cudaStream_t st)
+{
+    return e2m1 ? launch_quantize<true, Src, U>(src, chunks, codes, scales, st)
+                : launch_quantize<false, Src, U>(src, chunks, codes, scales, st);
 }
 
 cudaError_t launch_quantize_mx(const void* src, bool f32, long n, bool e2m1, uint8_t* codes,
                                uint8_t* scales, cudaStream_t st)
 {
     const long chunks = n / 8;
-    const dim3 grid((unsigned)((chunks + 255) / 256)), block(256);
-    if (f32) {
-        const float* s = static_cast<const float*>(src);
-        return e2m1 ? launch_pdl(quantize_kernel<true, float>, grid, block, 0, st, s, chunks, codes, scales)
-                    : launch_pdl(quantize_kernel<false, float>, grid, block, 0, st, s, chunks, codes, scales);
-    }
-    const uint16_t* s = static_cast<const uint16_t*>(src);
-    return e2m1 ? launch_pdl(quantize_kernel<true, uint16_t>, grid, block, 0, st, s, chunks, codes, scales)
-                : launch_pdl(quantize_kernel<false, uint16_t>, grid, block, 0, st, s, chunks, codes, scales);
+    // A grid that does not fill the SMs gains nothing from longer threads.
+    const bool many = chunks > 2048L * 4 * device_sms();
+    if (f32)
+        return many ? launch_quantize<float, 2>(src, chunks, e2m1, codes, scales, st)
+                    : launch_quantize<float, 1>(src, chunks, e2m1, codes, scales, st);
+    return many ? launch_quantize<uint16_t, 4>(src, chunks, e2m1, codes, scales, st)
+                : launch_quantize<uint16_t, 1>(src, chunks, e2m1, codes, scales, st);
 }
 
 }  // namespace moe

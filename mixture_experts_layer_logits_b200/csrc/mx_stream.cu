@@ -35,7 +35,8 @@ using gemm::silu_mul;
 
 constexpr int kSfBytes = 512 + 1024;      // scales of the token rows and of the weight rows
 constexpr int kTmemCols = 512;
-constexpr int kSfCol0 = 256;              // after the accumulator columns
+constexpr int kAccCols = 192;             // two accumulators of up to 192 columns, or one of 256
+constexpr int kSfCol0 = 2 * kAccCols;     // first scale column
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kScaleWarpB = 12, kGatherWarp0 = 14, kGatherWarps = 2;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);  // whole warpgroups; MODE 1 leaves two warps idle
 constexpr int kMaxStages = 6;
@@ -136,9 +137,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         aux->abort = 1;
     };
     // Weight rows per tile, 256, 192 or 128: the fewest rounds of the grid, each as long as its
-    // rows take to stream (fewer than about 178 rows take no less: the MMAs of a stage need 525
-    // cycles whatever N, as long as 178 rows take from HBM).  T = 8, E = 128, k = 8,
-    // I = 768: 52 experts x 6 tiles of 256 are 3 rounds, x 8 of 192 also, a quarter shorter.
+    // rows take to stream.  Per K tile that is about 2.95 cycles a row (all SMs sharing
+    // HBM), and no less than 525, which the MMAs and the scale copies take whatever N.
+    // T = 8, E = 128, k = 8, I = 768: 52 experts x 6 tiles of 256 are 3 rounds, x 8 of 192 also,
+    // a quarter shorter.  One accumulator of 256 columns cannot take the next tile's MMAs
+    // while it is read out, two of 192 can.
     const int tiles = groups.first[g.E];
     int nsel = 0;
     {
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int n = C::kMaxN - 64 * nsel;               // weight rows per tile
     const int features = MODE == 0 ? n / 2 : n;    // output features per tile
-    const int nbuf = n == 128 ? 2 : 1;             // accumulators that fit 256 columns
+    const int nbuf = n <= kAccCols ? 2 : 1;        // accumulators in flight
     const int fbs = nsel == 0 ? g.fb_count[0] : nsel == 1 ? g.fb_count[1] : g.fb_count[2];
     const uint32_t fb_magic = nsel == 0 ? g.fb_magic[0] : nsel == 1 ? g.fb_magic[1] : g.fb_magic[2];
     const int unit0 = (int)blockIdx.x, stride = (int)gridDim.x, units = tiles * fbs;
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = warp_agrees(mbar_wait(&aux->tempty[b], (uint32_t)(use & 1) ^ 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const uint32_t d = tmem_base + (uint32_t)(b * 128);
+            const uint32_t d = tmem_base + (uint32_t)(b * kAccCols);
             for (int kt = 0; kt < num_kt; ++kt) {
                 ok = warp_agrees(mbar_wait(&aux->full[stage], phase, abort_flag));
                 if (!ok) break;
@@ -404,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * 128);
+            const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * kAccCols);
             const int f0 = t.fb * features;
             if (lq * 32 < t.rows) {  // warp-uniform
                 if constexpr (MODE == 0) {
