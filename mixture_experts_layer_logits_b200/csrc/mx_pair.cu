@@ -37,6 +37,9 @@ using gemm::silu_mul;
 
 constexpr int kBM = 128;                  // weight rows of one CTA's tile
 constexpr int kATile = kBM * kBK;
+// weight rows of one TMA box (MODE 0 loads gate and up rows of 32 features in turn)
+template <int MODE>
+constexpr int kWBoxRows = MODE == 0 ? 32 : kBM;
 constexpr int kNT = 208;                  // the most token rows of a tile
 constexpr int kBRows = kNT / 2;           // token rows in one CTA's B tile
 constexpr int kBTile = kBRows * kBK;
@@ -68,6 +71,7 @@ struct Cfg {
 struct Aux {
     uint64_t full[kStages];
     uint64_t empty[kStages];
+    uint64_t gathered[kStages];  // MODE 0: this CTA's gathered rows of the stage have landed
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t drain;
@@ -172,10 +176,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            // CTA 0's counts: the expect_tx, and from both CTAs one arrival per warp of a scale
-            // team and per gather warp
-            mbar_init(&aux->full[s], 1 + 2 * (2 + (MODE == 0 ? kGatherWarps : 0)));
+            // CTA 0's counts: the expect_tx, one arrival per warp of a scale team from both CTAs, and
+            // CTA 1's relayed one for its gathered rows
+            mbar_init(&aux->full[s], 1 + 2 * 2 + (MODE == 0 ? 1 : 0));
             mbar_init(&aux->empty[s], 1);
+            mbar_init(&aux->gathered[s], kGatherWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&aux->tfull[b], 1);
@@ -231,6 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t tpol = l2_policy_evict_last();  // token rows are read again per feature block
         const uint32_t ring0 = smem_u32(ring);
         const uint32_t bytes = 2 * (kBM * kRowTx + (MODE == 1 ? kBTile : 0));
+        const uint32_t full0 = in_leader(&aux->full[0]);
         int stage = 0, fills = 0, e = 0;
         uint32_t phase = 0;
         bool ok = true, dep = !(MODE == 1 && g.early);
@@ -243,11 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = warp_agrees(mbar_wait(&aux->empty[stage], phase ^ 1u, abort_flag));
                 if (!ok) break;
                 const uint32_t st = ring0 + stage * kStageBytes;
-                const uint32_t bar = in_leader(&aux->full[stage]);
+                const uint32_t bar = full0 + stage * 8;
                 if (elect_one()) {
                     if (rank == 0) mbar_arrive_expect_tx(&aux->full[stage], bytes);
 #pragma unroll
-                    for (int r = 0; r < kBM; r += kWBox<MODE>)
+                    for (int r = 0; r < kBM; r += kWBoxRows<MODE>)
                         tma_2d<2>(st + r * kBK, &tm_w, bar, kt * kBK,
                                   row + (MODE == 0 ? tile_feature(r) + (tile_row_is_up(r) ? g.N : 0) : r), wpol);
                 }
@@ -279,7 +285,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (warp == 1 && rank == 0) {
+    } else if (warp == 1 && rank == 1) {
+        // ------------------------------------------------------------ relay (MODE 0)
+        // CTA 0 issues the MMAs of both: tell it when a stage's gathered rows are here.
+        if (MODE == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int u = unit0; u < units && ok; u += stride)
+                for (int kt = 0; kt < num_kt; ++kt) {
+                    ok = warp_agrees(mbar_wait(&aux->gathered[stage], phase, abort_flag));
+                    if (!ok) break;
+                    if (elect_one()) {
+                        fence_proxy_async_smem();
+                        arrive_leader(&aux->full[stage]);
+                    }
+                    __syncwarp();
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            if (!ok && lane == 0) flag_error();
+        }
+    } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         int stage = 0, lu = 0, e = 0;
         uint32_t phase = 0;
@@ -295,7 +324,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t d = tmem_base + (uint32_t)(b * kNT);
             const uint32_t idesc = idesc_formats(true) | idesc_shape(2 * kBM, n);
             for (int kt = 0; kt < num_kt; ++kt) {
-                ok = warp_agrees(mbar_wait_cluster(&aux->full[stage], phase, abort_flag));
+                ok = warp_agrees((MODE == 1 || mbar_wait(&aux->gathered[stage], phase, abort_flag)) &&
+                                 mbar_wait_cluster(&aux->full[stage], phase, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t sa = ring0 + stage * kStageBytes;
@@ -304,6 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t da = umma_desc_sw128(sa), db = umma_desc_sw128(sb);
                 const uint64_t ds = scale_desc(sf);
                 if (elect_one()) {
+                    if (MODE == 0) fence_proxy_async_smem();  // this CTA's rows came by cp.async
                     scales_to_tmem<2>(tsf, ds);
                     scales_to_tmem<2>(tsf + 4, ds + (512 >> 4));
                     if (n > 128) scales_to_tmem<2>(tsf + 8, ds + (1024 >> 4));
@@ -384,11 +415,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (MODE == 0 && warp >= kGatherWarp0) {
         // ------------------------------------------------------------ gather (MODE 0)
         // Thread i copies the 16-byte chunks i, i + 64, ... of this CTA's token rows (8 chunks a
-        // row).  The copies cannot arrive on the other CTA's barrier themselves, so a warp
-        // waits for its copies of kLag stages ago, fences them towards the async proxy and
-        // arrives there.
-        constexpr int kLag = 3;
-        static_assert(kLag < kStages, "a stage is filled before its ring slot comes round");
+        // row).  The copies arrive on this CTA's own barrier when they land (they cannot on the
+        // other CTA's); CTA 0's MMA warp waits for that, CTA 1's warp 1 relays it.
         const int i0 = threadIdx.x - kGatherWarp0 * 32;
         const uint64_t pol = l2_policy_evict_last();
         int q = 0, e = 0;
@@ -406,11 +434,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!debug_in_range(r[i], 0, g.R, g.err)) r[i] = 0;
                 }
             }
-        };
-        auto arrive = [&](int stage) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) arrive_leader(&aux->full[stage]);
         };
         next_rows(unit0);
         for (int u = unit0; u < units && ok; u += stride) {
@@ -435,16 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (src[i])
                         cp_async_16_hint(sb + j * 128 + (((c & 7) ^ (j & 7)) << 4), src[i] + kt * kBK, pol);
                 }
-                cp_async_commit();
-                if (q >= kLag) {
-                    cp_async_wait<kLag>();
-                    arrive((q - kLag) % kStages);
-                }
+                cp_async_mbar_arrive(&aux->gathered[stage]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&aux->gathered[stage]);
             }
         }
         cp_async_commit();
         cp_async_wait<0>();  // no copy is still in flight when the CTA exits
-        for (int p = max(q - kLag, 0); p < q && ok; ++p) arrive(p % kStages);
     } else if (warp >= kEpiWarp0 && warp < kEpiWarp0 + kEpiWarps) {
         // ------------------------------------------------------------ epilogue
         const int grp = (warp - kEpiWarp0) >> 2;     // token-column group
@@ -633,7 +653,7 @@ cudaError_t launch_mode(MxArgs g, cudaStream_t st)
     g.fb_magic[0] = magic(g.fb_count[0]);
     CUtensorMap tw, ta;
     cudaError_t e = weights_map(&tw, g.w, (uint64_t)g.E * g.N * (MODE == 0 ? 2 : 1), (uint64_t)g.K,
-                                kWBox<MODE>);
+                                kWBoxRows<MODE>);
     if (e == cudaSuccess)
         e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, kBRows, kBK)
                       : (ta = tw, e);
