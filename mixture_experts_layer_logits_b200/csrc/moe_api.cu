@@ -646,7 +646,12 @@ moe_status_t moe_forward_mx4(const uint8_t* x, const uint8_t* x_scale, const flo
     int32_t* offs = expert_offsets ? expert_offsets : at<int32_t>(ws, L.route.offsets);
     int32_t* rows = permuted_rows ? permuted_rows : at<int32_t>(ws, L.route.rows);
     void* y = at<void>(ws, L.y);
-    moe_status_t r = run_permute(logits, ids, wts, s, offs, rows, ws, L.route, st);
+    moe_status_t r = MOE_OK;
+    // The multi-CTA permutation tells its calls apart by a generation that a captured graph
+    // repeats; cleared, a replay cannot take the one before for its own.
+    if (s.T * (long long)s.top_k > kSmallRows)
+        r = cuda_status(cudaMemsetAsync(at<void>(ws, L.route.bar), 0, sizeof(GridBar), st));
+    if (r == MOE_OK) r = run_permute(logits, ids, wts, s, offs, rows, ws, L.route, st);
     if (r == MOE_OK)
         r = run_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, offs, rows, s, y, ws, L, st);
     if (r == MOE_OK) r = cuda_status(launch_combine(y, wts, s.T, s.top_k, s.H, out, st));

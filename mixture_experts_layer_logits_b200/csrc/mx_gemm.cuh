@@ -37,7 +37,6 @@ constexpr int kMaxExperts = 1024;
 template <int MODE>
 constexpr int kWBox = MODE == 0 ? 32 : 64;
 constexpr int kRowTx = kBK / 2;             // an unpacking TMA load counts its packed bytes
-constexpr int kScaleStages = 5;             // the fewest ring stages that run_scale_team allows
 constexpr int kSfCols = 16;                 // TMEM columns per stage for scales: 4 + 8 used
 constexpr int kTableBytes = 2 * (kMaxExperts + 1) * 4 + 120;
 
@@ -274,93 +273,88 @@ __device__ __forceinline__ uint32_t scale_place(int r)
 __device__ __forceinline__ int tile_feature(int r) { return r / 64 * 32 + r % 32; }
 __device__ __forceinline__ bool tile_row_is_up(int r) { return r / 32 % 2; }
 
-// One team of 64 threads that brings scales into the ring.  Reading 4 bytes a row and K tile
-// costs one L1 line lookup each, so a row is read a group of 4 K tiles at a time (16 bytes
-// where the row pitch allows it) into registers, one of the team's groups ahead, and stored
-// 4 bytes a stage.  A stage costs a team about 600 cycles (stores, the fence towards
-// tcgen05.cp's proxy, the arrival, the loads), so two teams take the groups in turn.  A team
-// steps over the other's group of 4 stages, and a wait on a ring slot must not be two
-// rounds ahead of the slot: that takes more than 4 stages (kScaleStages).
+// The kScaleWarps warps that bring scales into the ring.  Reading 4 bytes a row and K tile costs one
+// L1 line lookup and a 32-byte sector each time, so a row is read a group of 8 K tiles at a
+// time (32 bytes; in 16-byte loads where the row pitch allows it) into registers, one group
+// ahead, and stored 4 bytes a stage.  The rows are split over four warps because a stage costs a
+// warp some 200 cycles whatever it stores (the fence towards tcgen05.cp's proxy, the arrival);
+// two teams of two warps that took groups of 4 K tiles in turn, 16 bytes a row, fetched each
+// sector twice: prefill 1.27 ms instead of SCALEFIG.
+//   units       unit0, unit0 + stride, ... below `units`, each of num_kt K tiles
 //   kRows       rows of this thread; put[i]: where row i's bytes go within a stage's scales,
 //               or -1
+//   fetch(u)    starts reading what sources(u) needs
 //   sources(u, src)  sets the rows' first scale bytes for unit u
 //   wait(q)     waits until ring fill q may be written (false: give up)
 //   stage(q)    shared memory of that fill's scales
 //   arrive(q)   called by every lane after its warp's stores are fenced
-template <int kRows, typename Sources, typename Wait, typename Stage, typename Arrive>
-__device__ __forceinline__ void run_scale_team(int team, int unit0, int stride, int units, int num_kt,
-                                               int row_bytes, const int (&put)[kRows], Sources sources,
-                                               Wait wait, Stage stage, Arrive arrive)
+constexpr int kScaleWarps = 4;
+template <int kRows, typename Fetch, typename Sources, typename Wait, typename Stage, typename Arrive>
+__device__ __forceinline__ void run_scales(int unit0, int stride, int units, int num_kt, int row_bytes,
+                                           const int (&put)[kRows], Fetch fetch, Sources sources, Wait wait,
+                                           Stage stage, Arrive arrive)
 {
+    if (unit0 >= units) return;
     const int align = row_bytes & 15;  // 0: 16-byte rows, 8: 8-byte, else 4-byte
-    const int groups = (num_kt + 3) / 4;
     const uint8_t* src[kRows];
-    // the reader's place: unit, group in the unit, the unit that src belongs to
-    int ru = unit0, rg = team, have = -1;
-    auto settle = [&] {
-        while (rg >= groups && ru < units) {
-            rg -= groups;
-            ru += stride;
-        }
-    };
-    auto read = [&](uint32_t (&w)[kRows][4]) {
-        if (ru >= units) return;
-        if (have != ru) {
-            sources(ru, src);
-            have = ru;
-        }
-        const int kt = rg * 4;
+    uint32_t next[kRows][8];
+    auto read = [&](int kt) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            const uint8_t* p = src[i] + kt * 4;
+            if (put[i] < 0) continue;
+            const uint8_t* s = src[i] + kt * 4;
             if (align == 0) {
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-                w[i][0] = v.x, w[i][1] = v.y, w[i][2] = v.z, w[i][3] = v.w;
+#pragma unroll
+                for (int j = 0; j < 8; j += 4)
+                    if (kt + j < num_kt) {
+                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(s + 4 * j));
+                        next[i][j] = v.x, next[i][j + 1] = v.y, next[i][j + 2] = v.z, next[i][j + 3] = v.w;
+                    }
             } else if (align == 8) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-                w[i][0] = v.x, w[i][1] = v.y;
-                if (kt + 2 < num_kt) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2*>(p) + 1);
-                    w[i][2] = x.x, w[i][3] = x.y;
-                }
+#pragma unroll
+                for (int j = 0; j < 8; j += 2)
+                    if (kt + j < num_kt) {
+                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s + 4 * j));
+                        next[i][j] = v.x, next[i][j + 1] = v.y;
+                    }
             } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (kt + j < num_kt) w[i][j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+                for (int j = 0; j < 8; ++j)
+                    if (kt + j < num_kt) next[i][j] = __ldg(reinterpret_cast<const uint32_t*>(s + 4 * j));
             }
         }
-        rg += 2;
-        settle();
     };
-    uint32_t next[kRows][4];
-    settle();
-    int u = ru, grp = rg, lu = (ru - unit0) / stride;  // the writer's place
-    read(next);
-    while (u < units) {
-        uint32_t cur[kRows][4];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) cur[i][j] = next[i][j];
-        read(next);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (grp * 4 + j >= num_kt) break;
-            const int q = lu * num_kt + grp * 4 + j;
-            if (!wait(q)) return;
-            uint8_t* const sf = stage(q);
+    fetch(unit0);
+    sources(unit0, src);
+    read(0);
+    int q = 0;
+    for (int u = unit0; u < units; u += stride) {
+        if (u + stride < units) fetch(u + stride);
+        for (int kt = 0; kt < num_kt; kt += 8) {
+            uint32_t cur[kRows][8];
 #pragma unroll
             for (int i = 0; i < kRows; ++i)
-                if (put[i] >= 0) *reinterpret_cast<uint32_t*>(sf + put[i]) = cur[i][j];
-            fence_proxy_async_smem();
-            __syncwarp();
-            arrive(q);
-        }
-        grp += 2;
-        while (grp >= groups) {
-            grp -= groups;
-            u += stride;
-            ++lu;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) cur[i][j] = next[i][j];
+            if (kt + 8 < num_kt) {
+                read(kt + 8);
+            } else if (u + stride < units) {
+                sources(u + stride, src);
+                read(0);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (kt + j >= num_kt) break;
+                if (!wait(q)) return;
+                uint8_t* const sf = stage(q);
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (put[i] >= 0) *reinterpret_cast<uint32_t*>(sf + put[i]) = cur[i][j];
+                fence_proxy_async_smem();
+                __syncwarp();
+                arrive(q);
+                ++q;
+            }
         }
     }
 }

@@ -10,8 +10,8 @@
 // bound by L2 (11.5 TB/s of operand reads) at 2.11 ms for T = 8192, E = 128, k = 8, H = 4096,
 // I = 1536.
 //
-// Warp roles: 0 TMA; 1 TMEM, and in CTA 0 MMA issue for both; 2-3 and 12-13 scales (two
-// teams); 4-11 epilogue; MODE 0: 14-15 gather of token rows.
+// Warp roles: 0 TMA; 1 TMEM, and in CTA 0 MMA issue for both; 2-3 and 12-13
+// scales; 4-11 epilogue; MODE 0: 14-15 gather of token rows.
 //   - MODE 1 loads token rows by TMA with the weights; MODE 0 gathers x rows with 16-byte
 //     cp.async copies straight to their swizzled places.  (26 gather4 TMA loads a stage, one
 //     per lane, issue too slowly: w13 took 1.70 ms instead of 0.97.)
@@ -46,11 +46,10 @@ constexpr int kBTile = kBRows * kBK;
 constexpr int kSfBytes = 512 + 1024;      // scales of the weight rows and of all token rows
 constexpr int kStageBytes = (kATile + kBTile + kSfBytes + 1023) & ~1023;
 constexpr int kStages = 6;
-static_assert(kStages >= kScaleStages, "ring");
 constexpr int kTmemCols = 512;            // 2 accumulators of 208 columns, 6 x 16 of scales
 constexpr int kSfCol0 = 2 * kNT;
 static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "TMEM");
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kScaleWarpB = 12, kGatherWarp0 = 14, kGatherWarps = 2;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGatherWarp0 = 14, kGatherWarps = 2;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);  // whole warpgroups; MODE 1 leaves two warps idle
 constexpr int kGroupCols = kNT / 2;       // token columns per epilogue group of four warps
 // epilogue shared memory per warp: MODE 0, 2 buffers of 8 columns x 32 lanes of fp32 to swap, and 2
@@ -176,9 +175,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            // CTA 0's counts: the expect_tx, one arrival per warp of a scale team from both CTAs, and
-            // CTA 1's relayed one for its gathered rows
-            mbar_init(&aux->full[s], 1 + 2 * 2 + (MODE == 0 ? 1 : 0));
+            // CTA 0's counts: the expect_tx, one arrival per scale warp of both CTAs, and CTA 1's
+            // relayed one for its gathered rows
+            mbar_init(&aux->full[s], 1 + 2 * kScaleWarps + (MODE == 0 ? 1 : 0));
             mbar_init(&aux->empty[s], 1);
             mbar_init(&aux->gathered[s], kGatherWarps);
         }
@@ -359,48 +358,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         volatile int never = 0;
         if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
-    } else if (warp == 2 || warp == 3 || warp == kScaleWarpB || warp == kScaleWarpB + 1) {
+    } else if (warp == 2 || warp == 3 || warp == 12 || warp == 13) {
         // ------------------------------------------------------------ scales
-        // Thread i of a team handles weight rows i and i + 64 of this CTA's tile and token rows
-        // i, i + 64, ... of the whole tile (each CTA needs them all).
-        const int team = warp >= kScaleWarpB;
-        const int i0 = (team ? warp - kScaleWarpB : warp - 2) * 32 + lane;
+        // Thread i handles weight row i of this CTA's tile and token rows i and i + 128 of the
+        // whole tile (each CTA needs them all).
+        const int i0 = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
         const size_t ld = (size_t)g.K / 32;
         if (MODE == 1 && g.early) pdl_wait();  // act's scales
-        constexpr int kRows = 2 + 4;
-        int put[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = i0 + (i < 2 ? i : i - 2) * 64;
-            put[i] = i < 2 ? (int)scale_place(r) : r < kNT ? (int)(512 + scale_place(r)) : -1;
-        }
-        int e = 0;
-        auto sources = [&](int u, const uint8_t* (&src)[kRows]) {
-            const Unit t = unit(u, e);
-            const int f = first_feature(t);
+        constexpr int kRows = 3;
+        const int put[kRows] = {(int)scale_place(i0), (int)(512 + scale_place(i0)),
+                                i0 + 128 < kNT ? (int)(512 + scale_place(i0 + 128)) : -1};
+        int e = 0, tok[2];
+        Unit next;
+        auto fetch = [&](int u) {
+            next = unit(u, e);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                // MODE 1: rows past N belong to features that are never stored
-                const int r = i0 + i * 64;
-                const int row = MODE == 0 ? t.expert * 2 * g.N + f + tile_feature(r) +
-                                                (tile_row_is_up(r) ? g.N : 0)
-                                          : t.expert * g.N + min(f + r, g.N - 1);
-                src[i] = g.w_scale + (size_t)row * ld;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
                 // past the tile's end any scale will do
-                int r = t.row + min(i0 + i * 64, t.rows - 1);
+                tok[i] = next.row + min(i0 + i * 128, next.rows - 1);
                 if (MODE == 0) {
-                    r = g.rows[r];
-                    if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
-                    r = div_by(r, g.k, g.k_magic);
+                    tok[i] = g.rows[tok[i]];
+                    if (!debug_in_range(tok[i], 0, g.R, g.err)) tok[i] = 0;
                 }
-                src[2 + i] = g.a_scale + (size_t)r * ld;
             }
         };
-        run_scale_team<kRows>(
-            team, unit0, stride, units, num_kt, (int)ld, put, sources,
+        auto sources = [&](int, const uint8_t* (&src)[kRows]) {
+            // MODE 1: rows past N belong to features that are never stored
+            const int f = first_feature(next);
+            const int row = MODE == 0 ? next.expert * 2 * g.N + f + tile_feature(i0) +
+                                            (tile_row_is_up(i0) ? g.N : 0)
+                                      : next.expert * g.N + min(f + i0, g.N - 1);
+            src[0] = g.w_scale + (size_t)row * ld;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                src[1 + i] = g.a_scale + (size_t)(MODE == 0 ? div_by(tok[i], g.k, g.k_magic) : tok[i]) * ld;
+        };
+        run_scales<kRows>(
+            unit0, stride, units, num_kt, (int)ld, put, fetch, sources,
             [&](int q) {
                 const bool ok = warp_agrees(mbar_wait(&aux->empty[q % kStages],
                                                                   (uint32_t)((q / kStages) & 1) ^ 1u,

@@ -15,7 +15,7 @@
 // One accumulator lane is one token, so a thread holds a token's features in its columns: SwiGLU,
 // the MX blocks of act and the rows of y need no exchange between threads.
 //
-// Warp roles: 0 TMA; 1 TMEM and MMA issue; 2-3 and 12-13 scales (two teams); 4-11 epilogue;
+// Warp roles: 0 TMA; 1 TMEM and MMA issue; 2-3 and 12-13 scales; 4-11 epilogue;
 // MODE 0: 14-15 gather of token rows (16-byte cp.async copies).
 // Every mbarrier wait is bounded; on a timeout the kernel records the error word, stops
 // issuing, drains what it issued and frees TMEM.
@@ -37,7 +37,7 @@ constexpr int kSfBytes = 512 + 1024;      // scales of the token rows and of the
 constexpr int kTmemCols = 512;
 constexpr int kAccCols = 192;             // two accumulators of up to 192 columns, or one of 256
 constexpr int kSfCol0 = 2 * kAccCols;     // first scale column
-constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kScaleWarpB = 12, kGatherWarp0 = 14, kGatherWarps = 2;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGatherWarp0 = 14, kGatherWarps = 2;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);  // whole warpgroups; MODE 1 leaves two warps idle
 constexpr int kMaxStages = 6;
 
@@ -55,10 +55,9 @@ struct Cfg {
     static constexpr int kStages = kStagesRaw > kMaxStages ? kMaxStages : kStagesRaw;
     static constexpr int kSmem = kFixed + kStages * kStageBytes;
     static constexpr int kGIters = (NT * 8 + kGatherWarps * 32 - 1) / (kGatherWarps * 32);
-    static constexpr int kSIters = (NT + 63) / 64;
     static_assert(kATile + kBTile >= 128 * kBK, "the M operand's 128 rows lie inside the stage");
     static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "TMEM");
-    static_assert(kStages >= kScaleStages && NT % 16 == 0 && NT <= 128, "tile");
+    static_assert(kStages >= 4 && NT % 16 == 0 && NT <= 128, "tile");
 };
 
 struct Aux {
@@ -102,8 +101,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::kStages; ++s) {
-            // the expect_tx, one arrival per warp of a scale team and per gather warp
-            mbar_init(&aux->full[s], 1 + 2 + (MODE == 0 ? kGatherWarps : 0));
+            // the expect_tx, one arrival per scale warp and per gather warp
+            mbar_init(&aux->full[s], 1 + kScaleWarps + (MODE == 0 ? kGatherWarps : 0));
             mbar_init(&aux->empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -273,54 +272,41 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         volatile int never = 0;
         if (!mbar_wait(&aux->drain, 0, &never, 500000000ull)) atomicExch(g.err, kDeviceErrorMagic);
-    } else if (warp == 2 || warp == 3 || warp == kScaleWarpB || warp == kScaleWarpB + 1) {
+    } else if (warp == 2 || warp == 3 || warp == 12 || warp == 13) {
         // ------------------------------------------------------------ scales
-        // Thread i of a team handles weight rows i, i + 64, ... of the tile and token rows i, ...
-        const int team = warp >= kScaleWarpB;
-        const int i0 = (team ? warp - kScaleWarpB : warp - 2) * 32 + lane;
+        // Thread i handles weight rows i and i + 128 of the tile and token row i.
+        const int i0 = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
         const size_t ld = (size_t)g.K / 32;
         if (MODE == 1 && g.early) pdl_wait();  // act's scales
-        constexpr int kW = C::kMaxN / 64, kRows = kW + C::kSIters;
-        int put[kRows];
-#pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = i0 + (i < kW ? i : i - kW) * 64;
-            if (i < kW)
-                put[i] = r < n ? (int)(512 + scale_place(r)) : -1;
-            else
-                put[i] = r < NT ? (int)scale_place(r) : -1;
-        }
-        int e = 0;
-        auto sources = [&](int u, const uint8_t* (&src)[kRows]) {
-            const Unit t = unit(u, e);
-            const int f = t.fb * features;
-#pragma unroll
-            for (int i = 0; i < kW; ++i) {
-                // rows past the expert's last belong to features that are never stored
-                const int r = i0 + i * 64;
-                int row;
-                if (MODE == 0) {
-                    row = t.expert * 2 * g.N + min(f + tile_feature(r), g.N - 1) +
-                          (tile_row_is_up(r) ? g.N : 0);
-                } else {
-                    row = t.expert * g.N + min(f + r, g.N - 1);
-                }
-                src[i] = g.w_scale + (size_t)row * ld;
-            }
-#pragma unroll
-            for (int i = 0; i < C::kSIters; ++i) {
-                // past the tile's end any scale will do
-                int r = t.row + min(i0 + i * 64, t.rows - 1);
-                if (MODE == 0) {
-                    r = g.rows[r];
-                    if (!debug_in_range(r, 0, g.R, g.err)) r = 0;
-                    r = div_by(r, g.k, g.k_magic);
-                }
-                src[kW + i] = g.a_scale + (size_t)r * ld;
+        constexpr int kRows = 3;
+        const int put[kRows] = {(int)(512 + scale_place(i0)), i0 + 128 < n ? (int)(512 + scale_place(i0 + 128)) : -1,
+                                i0 < NT ? (int)scale_place(i0) : -1};
+        int e = 0, tok;
+        Unit next;
+        auto fetch = [&](int u) {
+            next = unit(u, e);
+            // past the tile's end any scale will do
+            tok = next.row + min(i0, next.rows - 1);
+            if (MODE == 0) {
+                tok = g.rows[tok];
+                if (!debug_in_range(tok, 0, g.R, g.err)) tok = 0;
             }
         };
-        run_scale_team<kRows>(
-            team, unit0, stride, units, num_kt, (int)ld, put, sources,
+        auto sources = [&](int, const uint8_t* (&src)[kRows]) {
+            // rows past the expert's last belong to features that are never stored
+            const int f = next.fb * features;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int r = i0 + i * 128;
+                const int row = MODE == 0 ? next.expert * 2 * g.N + min(f + tile_feature(r), g.N - 1) +
+                                                (tile_row_is_up(r) ? g.N : 0)
+                                          : next.expert * g.N + min(f + r, g.N - 1);
+                src[i] = g.w_scale + (size_t)row * ld;
+            }
+            src[2] = g.a_scale + (size_t)(MODE == 0 ? div_by(tok, g.k, g.k_magic) : tok) * ld;
+        };
+        run_scales<kRows>(
+            unit0, stride, units, num_kt, (int)ld, put, fetch, sources,
             [&](int q) {
                 const bool ok = warp_agrees(mbar_wait(&aux->empty[q % C::kStages],
                                                                   (uint32_t)((q / C::kStages) & 1) ^ 1u,

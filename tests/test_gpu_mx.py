@@ -169,6 +169,9 @@ MM = [
     ([5, 0, 31, 32, 33, 1], 376, 640), ([129, 64, 0, 255], 256, 128), ([300, 1, 0, 513], 520, 512),
     ([700, 33, 225, 0, 449], 384, 1152), ([2] * 200, 64, 128), ([40] * 9, 1160, 2176),
     ([0, 0, 4], 2048, 7168),
+    # experts with many rows (pairs of CTAs), each pitch of the scale rows, one and many K tiles
+    ([208], 256, 128), ([209, 300], 136, 768), ([416, 0, 1, 1000], 640, 512), ([150] * 7, 128, 2048),
+    ([257, 129], 2056, 896), ([2000], 384, 256),
 ]
 
 
@@ -186,11 +189,12 @@ def test_grouped_mm(counts, N, K):
     assert torch.equal(moe.moe_grouped_mm_mx4(a, sa, w, sw, off), y)
 
 
-def test_grouped_mm_small_integers_are_exact():
+@pytest.mark.parametrize("counts", [[77, 0, 126], [300, 0, 513]])
+def test_grouped_mm_small_integers_are_exact(counts):
     """Small whole numbers under scales of one: every product and sum is exact, so a wrong element,
     scale or place cannot hide inside a tolerance."""
     g = gen(9)
-    R, E, N, K = 203, 3, 264, 384
+    R, E, N, K = sum(counts), 3, 264, 384
     a = torch.randint(-4, 5, (R, K), generator=g, device="cuda")
     w = torch.randint(-4, 5, (E, N, K), generator=g, device="cuda")
     sa = torch.randint(125, 130, (R, K // 32), generator=g, device="cuda").to(U8)
@@ -200,16 +204,17 @@ def test_grouped_mm_small_integers_are_exact():
     _, pw = ref.round_to(w.to(ref.F64), "e2m1")
     cw = (pw | ((w < 0).long() << 3)).to(U8)
     cw = cw[..., 0::2] | (cw[..., 1::2] << 4)
-    off = offsets_of([77, 0, 126])
+    off = offsets_of(counts)
     y = moe.moe_grouped_mm_mx4(ca, sa, cw.contiguous(), sw, off)
     want, _ = ref.grouped_mm(ref.decode(ca, sa, "e4m3"), cw, sw, off)
     assert torch.equal(y, want.to(F32).to(BF16))   # the sums fit fp32 exactly
 
 
-def test_grouped_mm_leaves_rows_behind_the_last_group():
-    a, sa, w, sw = draw_mm(300, 4, 256, 256)
+@pytest.mark.parametrize("R", [300, 900])
+def test_grouped_mm_leaves_rows_behind_the_last_group(R):
+    a, sa, w, sw = draw_mm(R, 4, 256, 256)
     off = offsets_of([40, 0, 100, 3])
-    y = torch.full((300, 256), 7.0, dtype=BF16, device="cuda")
+    y = torch.full((R, 256), 7.0, dtype=BF16, device="cuda")
     moe.moe_grouped_mm_mx4(a, sa, w, sw, off, y=y)
     want, tol = ref.grouped_mm(ref.decode(a, sa, "e4m3"), w, sw, off)
     ref.assert_within(y[:143], want[:143], tol[:143], "y")
@@ -231,6 +236,20 @@ def test_grouped_mm_nan_blocks_stay_in_their_row_and_column():
     bad[7] = bad[41] = True
     bad[30:, 100] = True
     assert bool(torch.isnan(y[bad]).all()) and torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("R", [100, 700])
+def test_grouped_mm_offsets_out_of_contract_stay_inside(R):
+    """Offsets that descend or pass R are taken as empty or cut groups: nothing is read or written
+    outside the operands."""
+    a, sa, w, sw = draw_mm(R, 4, 136, 128)
+    buf, y = guarded((R, 136), BF16)
+    y.fill_(2.0)
+    off = torch.tensor([0, 50, 20, R + 500, R - 10], dtype=I32, device="cuda")
+    ws = torch.empty(moe.moe_grouped_mm_workspace_size(R, 4, 136, 128), dtype=U8, device="cuda")
+    moe.moe_grouped_mm_mx4(a, sa, w, sw, off, ws=ws, y=y)
+    moe.moe_grouped_mm_mx4(a, sa, w, sw, -off - 1, ws=ws, y=y)
+    assert moe.moe_device_status(ws) == moe.MOE_OK and intact(buf)
 
 
 def test_grouped_mm_extreme_scales():
