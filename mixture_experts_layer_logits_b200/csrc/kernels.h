@@ -265,8 +265,8 @@ struct MxArgs {
     int32_t* err;
     int E, R, k, N, K;
     // set by launch_mx_grouped
-    int fb_count[3];         // feature blocks of an expert, per tile width
-    uint32_t fb_magic[3];    // for divisions by them and by k
+    int fb_count;            // feature blocks of an expert
+    uint32_t fb_magic;       // for divisions by it and by k
     uint32_t k_magic;
     int early;               // only `a` comes from the launch before
     int stream_weights;      // weights are read once: evict first

@@ -40,39 +40,45 @@ constexpr int kATile = kBM * kBK;
 // weight rows of one TMA box (MODE 0 loads gate and up rows of 32 features in turn)
 template <int MODE>
 constexpr int kWBoxRows = MODE == 0 ? 32 : kBM;
-constexpr int kNT = 208;                  // the most token rows of a tile
-constexpr int kBRows = kNT / 2;           // token rows in one CTA's B tile
-constexpr int kBTile = kBRows * kBK;
-constexpr int kSfBytes = 512 + 1024;      // scales of the weight rows and of all token rows
-constexpr int kStageBytes = (kATile + kBTile + kSfBytes + 1023) & ~1023;
-constexpr int kStages = 6;
-constexpr int kTmemCols = 512;            // 2 accumulators of 208 columns, 6 x 16 of scales
-constexpr int kSfCol0 = 2 * kNT;
-static_assert(kSfCol0 + kStages * kSfCols <= kTmemCols, "TMEM");
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGatherWarp0 = 14, kGatherWarps = 2;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);  // whole warpgroups; MODE 1 leaves two warps idle
-constexpr int kGroupCols = kNT / 2;       // token columns per epilogue group of four warps
+constexpr int kMaxStages = 12;
 // epilogue shared memory per warp: MODE 0, 2 buffers of 8 columns x 32 lanes of fp32 to swap, and 2
 // of 8 token rows of 32 E4M3 codes (48 bytes apart: the rows that a store hits share no bank);
 // MODE 1, 2 buffers of 8 token rows x 32 bf16
 constexpr int kCodePitch = 48;
 constexpr int kWarpStaging = 2 * 1024 + 2 * 8 * kCodePitch;
 
-template <int MODE>
+// NT: the most token rows of a tile.
+template <int MODE, int NT>
 struct Cfg {
+    static constexpr int kBRows = NT / 2;                        // token rows in one CTA's B tile
+    static constexpr int kBTile = kBRows * kBK;
+    static constexpr int kTokenScales = NT > 128 ? 1024 : 512;   // bytes a stage
+    static constexpr int kStageBytes = (kATile + kBTile + 512 + kTokenScales + 1023) & ~1023;
     static constexpr int kStaging = kEpiWarps * (MODE == 0 ? kWarpStaging : 1024);
-    static constexpr int kSmem = 1024 + kStages * kStageBytes + kStaging + 512 + kTableBytes;
-    static constexpr int kFeatures = MODE == 0 ? 64 : 128;   // output features of one CTA
+    static constexpr int kFixed = 1024 + kStaging + 512 + kTableBytes;
+    static constexpr int kNBuf = NT <= 64 ? 4 : 2;               // accumulators in flight
+    static constexpr int kSfCol0 = kNBuf * NT;                   // first scale column
+    static constexpr int kSfCols = NT > 128 ? 16 : 8;            // per stage; 4 of weights, 4 or 8 of tokens
+    static constexpr int kStagesSmem = (232448 - kFixed) / kStageBytes;
+    static constexpr int kStagesTmem = (512 - kSfCol0) / kSfCols;
+    static constexpr int kStagesRaw = kStagesSmem < kStagesTmem ? kStagesSmem : kStagesTmem;
+    static constexpr int kStages = kStagesRaw < kMaxStages ? kStagesRaw : kMaxStages;
+    static constexpr int kSmem = kFixed + kStages * kStageBytes;
+    static constexpr int kTmemCols = kSfCol0 + kStages * kSfCols <= 256 ? 256 : 512;
+    static constexpr int kFeatures = MODE == 0 ? 64 : 128;       // output features of one CTA
+    static constexpr int kGroupCols = NT / 2;                    // token columns per epilogue group of four warps
     static constexpr int kGIters = (kBRows * 8 + kGatherWarps * 32 - 1) / (kGatherWarps * 32);
-    static_assert(kSmem <= 232448, "shared memory");
+    static_assert(NT % 16 == 0 && NT <= 256 && kStages >= 4 && kSmem <= 232448, "tile");
 };
 
 struct Aux {
-    uint64_t full[kStages];
-    uint64_t empty[kStages];
-    uint64_t gathered[kStages];  // MODE 0: this CTA's gathered rows of the stage have landed
-    uint64_t tfull[2];
-    uint64_t tempty[2];
+    uint64_t full[kMaxStages];
+    uint64_t empty[kMaxStages];
+    uint64_t gathered[kMaxStages];  // MODE 0: this CTA's gathered rows of the stage have landed
+    uint64_t tfull[4];
+    uint64_t tempty[4];
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
@@ -158,12 +164,14 @@ __device__ __forceinline__ void store_matrix_x4_trans(uint32_t addr, uint32_t a,
                  : "memory");
 }
 
-template <int MODE>
+template <int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                    const MxArgs g)
 {
-    using C = Cfg<MODE>;
+    using C = Cfg<MODE, NT>;
+    constexpr int kStages = C::kStages, kStageBytes = C::kStageBytes, kBTile = C::kBTile;
+    constexpr int kGroupCols = C::kGroupCols, kNBuf = C::kNBuf;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -181,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&aux->empty[s], 1);
             mbar_init(&aux->gathered[s], kGatherWarps);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kNBuf; ++b) {
             mbar_init(&aux->tfull[b], 1);
             mbar_init(&aux->tempty[b], 2 * kEpiWarps);
         }
@@ -194,7 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                          smem_u32(&aux->tmem_base)),
-                     "r"(kTmemCols)
+                     "r"(C::kTmemCols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
@@ -204,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!g.early) pdl_wait();
     pdl_launch_dependents();
     const Groups groups =
-        build_groups<kThreads>(g, kNT, reinterpret_cast<int*>(staging + C::kStaging + 512));
+        build_groups<kThreads>(g, NT, reinterpret_cast<int*>(staging + C::kStaging + 512));
     tc_fence_before();
     cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
     tc_fence_after();
@@ -218,10 +226,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         atomicExch(g.err, kDeviceErrorMagic);
         aux->abort = 1;
     };
-    const int fbs = g.fb_count[0];
+    const int fbs = g.fb_count;
     const int units = groups.first[g.E] * fbs;
     const int num_kt = g.K / kBK;
-    auto unit = [&](int u, int& e) { return groups.unit(u, fbs, g.fb_magic[0], e); };
+    auto unit = [&](int u, int& e) { return groups.unit(u, fbs, g.fb_magic, e); };
     auto padded = [](int rows) { return (rows + 15) & ~15; };  // the MMA's N
     // this CTA's part of a unit: its first output feature, and its first token row in the tile.
     // MODE 1: the second CTA's features may begin past N; it then works on the first ones
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        const uint64_t wpol = l2_policy_evict_normal();
+        const uint64_t wpol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
         const uint64_t tpol = l2_policy_evict_last();  // token rows are read again per feature block
         const uint32_t ring0 = smem_u32(ring);
         const uint32_t bytes = 2 * (kBM * kRowTx + (MODE == 1 ? kBTile : 0));
@@ -315,12 +323,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ring0 = smem_u32(ring);
         for (int u = unit0; u < units && ok; u += stride, ++lu) {
             const Unit t = unit(u, e);
-            const int b = lu & 1;
-            ok = warp_agrees(mbar_wait_cluster(&aux->tempty[b], (uint32_t)((lu >> 1) & 1) ^ 1u, abort_flag));
+            const int b = lu % kNBuf;
+            ok = warp_agrees(
+                mbar_wait_cluster(&aux->tempty[b], (uint32_t)((lu / kNBuf) & 1) ^ 1u, abort_flag));
             if (!ok) break;
             tc_fence_after();
             const int n = padded(t.rows);
-            const uint32_t d = tmem_base + (uint32_t)(b * kNT);
+            const uint32_t d = tmem_base + (uint32_t)(b * NT);
             const uint32_t idesc = idesc_formats(true) | idesc_shape(2 * kBM, n);
             for (int kt = 0; kt < num_kt; ++kt) {
                 ok = warp_agrees((MODE == 1 || mbar_wait(&aux->gathered[stage], phase, abort_flag)) &&
@@ -329,14 +338,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 const uint32_t sa = ring0 + stage * kStageBytes;
                 const uint32_t sb = sa + kATile, sf = sb + kBTile;
-                const uint32_t tsf = tmem_base + (uint32_t)(kSfCol0 + stage * kSfCols);
+                const uint32_t tsf = tmem_base + (uint32_t)(C::kSfCol0 + stage * C::kSfCols);
                 const uint64_t da = umma_desc_sw128(sa), db = umma_desc_sw128(sb);
                 const uint64_t ds = scale_desc(sf);
                 if (elect_one()) {
                     if (MODE == 0) fence_proxy_async_smem();  // this CTA's rows came by cp.async
                     scales_to_tmem<2>(tsf, ds);
                     scales_to_tmem<2>(tsf + 4, ds + (512 >> 4));
-                    if (n > 128) scales_to_tmem<2>(tsf + 8, ds + (1024 >> 4));
+                    if (NT > 128 && n > 128) scales_to_tmem<2>(tsf + 8, ds + (1024 >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along K
                         umma<2>(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
@@ -365,15 +374,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i0 = (warp < 4 ? warp - 2 : warp - 10) * 32 + lane;
         const size_t ld = (size_t)g.K / 32;
         if (MODE == 1 && g.early) pdl_wait();  // act's scales
-        constexpr int kRows = 3;
-        const int put[kRows] = {(int)scale_place(i0), (int)(512 + scale_place(i0)),
-                                i0 + 128 < kNT ? (int)(512 + scale_place(i0 + 128)) : -1};
-        int e = 0, tok[2];
+        constexpr int kTok = NT > 128 ? 2 : 1, kRows = 1 + kTok;
+        int put[kRows] = {(int)scale_place(i0)};
+#pragma unroll
+        for (int i = 0; i < kTok; ++i)
+            put[1 + i] = i0 + i * 128 < NT ? (int)(512 + scale_place(i0 + i * 128)) : -1;
+        int e = 0, tok[kTok];
         Unit next;
         auto fetch = [&](int u) {
             next = unit(u, e);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < kTok; ++i) {
                 // past the tile's end any scale will do
                 tok[i] = next.row + min(i0 + i * 128, next.rows - 1);
                 if (MODE == 0) {
@@ -390,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                       : next.expert * g.N + min(f + i0, g.N - 1);
             src[0] = g.w_scale + (size_t)row * ld;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+            for (int i = 0; i < kTok; ++i)
                 src[1 + i] = g.a_scale + (size_t)(MODE == 0 ? div_by(tok[i], g.k, g.k_magic) : tok[i]) * ld;
         };
         run_scales<kRows>(
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < C::kGIters; ++i) {
                 const int j = (i0 + i * kGatherWarps * 32) >> 3;
                 r[i] = -1;
-                if (j < kBRows && first_token(t) + j < t.rows) {
+                if (j < C::kBRows && first_token(t) + j < t.rows) {
                     r[i] = g.rows[t.row + first_token(t) + j];
                     if (!debug_in_range(r[i], 0, g.R, g.err)) r[i] = 0;
                 }
@@ -473,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lu = 0, e = 0;
         for (int u = unit0; u < units; u += stride, ++lu) {
             const Unit t = unit(u, e);
-            const int b = lu & 1;
+            const int b = lu % kNBuf;
             const int jend = min(t.rows, jbeg + kGroupCols);
             // MODE 1: lane i holds the y rows of the group's columns i, i + 32, ...
             int yrow[(kGroupCols + 31) / 32] = {};
@@ -487,13 +498,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu >> 1) & 1), abort_flag);
+            const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu / kNBuf) & 1), abort_flag);
             if (!got) flag_error();
             // same in all 4 warps; also: the group is done with the unit before's staging
             if (named_bar_or(1 + grp, 128, !got || *abort_flag)) break;
             __syncwarp();
             tc_fence_after();
-            const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * kNT);
+            const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * NT);
             if constexpr (MODE == 0) {
                 // Warps 0 and 2 of a group hold the gates of 32 features, an MX block of act, and
                 // warps 1 and 3 their ups.  Of every two column blocks the gate warp finishes the
@@ -634,32 +645,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base),
-                     "r"(kTmemCols)
+                     "r"(C::kTmemCols)
                      : "memory");
     }
 }
 
-template <int MODE>
-cudaError_t launch_mode(MxArgs g, cudaStream_t st)
+template <int MODE, int NT>
+cudaError_t launch_nt(MxArgs g, cudaStream_t st)
 {
-    using C = Cfg<MODE>;
-    g.fb_count[0] = (g.N + 2 * C::kFeatures - 1) / (2 * C::kFeatures);
-    g.fb_magic[0] = magic(g.fb_count[0]);
+    using C = Cfg<MODE, NT>;
+    g.fb_count = (g.N + 2 * C::kFeatures - 1) / (2 * C::kFeatures);
+    g.fb_magic = magic(g.fb_count);
     CUtensorMap tw, ta;
     cudaError_t e = weights_map(&tw, g.w, (uint64_t)g.E * g.N * (MODE == 0 ? 2 : 1), (uint64_t)g.K,
                                 kWBoxRows<MODE>);
     if (e == cudaSuccess)
-        e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, kBRows, kBK)
+        e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, C::kBRows, kBK)
                       : (ta = tw, e);
     if (e != cudaSuccess) return e;
-    return launch<mx_pair_kernel<MODE>>(device_sms() / 2 * 2, 2, kThreads, C::kSmem, st, tw, ta, g);
+    return launch<mx_pair_kernel<MODE, NT>>(device_sms() / 2 * 2, 2, kThreads, C::kSmem, st, tw, ta, g);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
+{
+    if (most <= 16) return launch_nt<MODE, 16>(g, st);
+    if (most <= 32) return launch_nt<MODE, 32>(g, st);
+    if (most <= 64) return launch_nt<MODE, 64>(g, st);
+    if (g.R < 64LL * g.E) return launch_nt<MODE, 128>(g, st);
+    return launch_nt<MODE, 208>(g, st);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_pair(const MxArgs& g, int mode, cudaStream_t st)
+cudaError_t launch_mx_grouped(const MxArgs& args, int mode, cudaStream_t st)
 {
-    return mode == 0 ? launch_mode<0>(g, st) : launch_mode<1>(g, st);
+    MxArgs g = args;
+    // the most rows that one expert can have: a token picks an expert at most once
+    const int most = mode == 2 ? g.R : g.R / g.k;
+    g.early = mode == 1;
+    g.stream_weights = most <= 64;
+    if (mode == 2) {
+        g.rows = nullptr;
+        g.k = 1;
+    }
+    g.k_magic = magic(g.k);
+    return mode == 0 ? launch_mode<0>(g, most, st) : launch_mode<1>(g, most, st);
 }
 
 }  // namespace moe
