@@ -208,16 +208,34 @@ struct Groups {
     }
 };
 
+// A thread's share of expert_offsets: those of experts threadIdx.x * kPer + i, and the next.
+// Read on their own so that their way from L2 passes under the rest of the prologue.
+template <int kThreads>
+struct Offsets {
+    static constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+    int v[kPer + 1];
+
+    __device__ __forceinline__ void read(const MxArgs& g)
+    {
+#pragma unroll
+        for (int i = 0; i <= kPer; ++i) {
+            const int e = threadIdx.x * kPer + i;
+            v[i] = e <= g.E ? __ldcg(g.offsets + e) : 0;
+        }
+    }
+};
+
 // Fills first / start (kTableBytes of shared memory at `tables`) for tiles of up to nt rows.
 // Offsets are clamped to 0 .. R and to ascending order, so that none leads outside the
 // operands.  All kThreads threads call it; it ends with a barrier.
 template <int kThreads>
-__device__ __forceinline__ Groups build_groups(const MxArgs& g, int nt, int* tables)
+__device__ __forceinline__ Groups build_groups(const MxArgs& g, const Offsets<kThreads>& off, int nt,
+                                               int* tables)
 {
     int* first = tables;
     int* start = tables + kMaxExperts + 1;
     int* warp_sum = start + kMaxExperts + 1;
-    constexpr int kPer = (kMaxExperts + kThreads - 1) / kThreads;
+    constexpr int kPer = Offsets<kThreads>::kPer;
     static_assert(kThreads / 32 * 4 <= 120, "warp_sum");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int tiles[kPer], sum = 0;
@@ -226,8 +244,8 @@ __device__ __forceinline__ Groups build_groups(const MxArgs& g, int nt, int* tab
         const int e = threadIdx.x * kPer + i;
         tiles[i] = 0;
         if (e < g.E) {
-            const int a = min(max(__ldcg(g.offsets + e), 0), g.R);
-            const int b = min(max(__ldcg(g.offsets + e + 1), a), g.R);
+            const int a = min(max(off.v[i], 0), g.R);
+            const int b = min(max(off.v[i + 1], a), g.R);
             start[e] = a;
             if (e == g.E - 1) start[g.E] = b;
             tiles[i] = (b - a + nt - 1) / nt;

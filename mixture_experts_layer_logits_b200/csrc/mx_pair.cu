@@ -95,11 +95,13 @@ __device__ __forceinline__ void commit(uint64_t* bar)
         : "memory");
 }
 
-__device__ __forceinline__ void cluster_sync()
+__device__ __forceinline__ void cluster_arrive()
 {
-    asm volatile(
-        "barrier.cluster.arrive.release;\n\t"
-        "barrier.cluster.wait.acquire;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // Address of the same shared-memory location in CTA 0 of the cluster.
@@ -181,6 +183,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+    // The second product of the FFN (g.early) takes only act from the launch before it;
+    // expert_offsets, rows and weights were complete before that launch passed its own
+    // wait, so the tables and the first weight tiles need not wait for it.
+    Offsets<kThreads> offsets;
+    if (g.early) offsets.read(g);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             // CTA 0's counts: the expect_tx, one arrival per scale warp of both CTAs, and CTA 1's
@@ -206,15 +213,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-    // The second product of the FFN (g.early) takes only act from the launch before it;
-    // expert_offsets, rows and weights were complete before that launch passed its own
-    // wait, so the tables and the first weight tiles need not wait for it.
-    if (!g.early) pdl_wait();
-    pdl_launch_dependents();
-    const Groups groups =
-        build_groups<kThreads>(g, NT, reinterpret_cast<int*>(staging + C::kStaging + 512));
     tc_fence_before();
-    cluster_sync();  // barriers initialised and TMEM allocated in both CTAs
+    cluster_arrive();  // barriers initialised, TMEM allocated
+    if (!g.early) {
+        pdl_wait();
+        offsets.read(g);
+    }
+    pdl_launch_dependents();
+    const Groups groups = build_groups<kThreads>(
+        g, offsets, NT, reinterpret_cast<int*>(staging + C::kStaging + 512));
+    cluster_wait();    // ... in the other CTA too
     tc_fence_after();
 
     uint32_t rank;
@@ -640,7 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     tc_fence_before();
-    cluster_sync();  // neither CTA leaves while the other may arrive on its barriers
+    cluster_arrive();
+    cluster_wait();  // neither CTA leaves while the other may arrive on its barriers
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
