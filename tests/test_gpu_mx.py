@@ -263,6 +263,53 @@ def test_grouped_mm_extreme_scales():
     ref.assert_within(y, want, tol, "y")
 
 
+# ------------------------------------------------------------------ past 32-bit offsets
+
+
+def test_norm_and_quantize_past_2_to_31_elements():
+    T, H = 70_001, 32_768
+    x = torch.empty(T, H, dtype=BF16, device="cuda")
+    for i in range(0, T, 10_000):
+        x[i:i + 10_000] = randn(min(10_000, T - i), H, g=gen(60 + i))
+    w = (1 + 0.1 * randn(H, g=gen(61))).to(BF16)
+    _, out, codes, scales = moe.moe_add_rmsnorm(x, w, quantize=True)
+    pick = torch.tensor([0, 1, 65_535, 65_536, T - 1], device="cuda")
+    _, n, err = ref.rmsnorm(x[pick], None, w, 1e-6)
+    ref.assert_within(out[pick], n, err + ref.BF16_HALF_STEP * (n.abs() + err), "out")
+    ref.assert_within(ref.decode(codes[pick], scales[pick], "e4m3"), ref.mx(n), ref.mx_shift(n, err),
+                      "codes")
+    for fmt in ("e2m1", "e4m3"):
+        codes, scales = moe.moe_quantize_mx(x, fmt)
+        want = ref.quantize(x[pick].to(ref.F64), fmt)
+        assert torch.equal(codes[pick], want[0]) and torch.equal(scales[pick], want[1])
+
+
+def test_grouped_mm_output_past_2_to_31_elements():
+    counts, N, K = [30_000, 3, 39_998], 32_776, 128
+    R = sum(counts)
+    a, sa = moe.moe_quantize_mx(randn(R, K, g=gen(62)).to(BF16), "e4m3")
+    w, sw = moe.moe_quantize_mx(randn(3, N, K, g=gen(63)).to(BF16))
+    y = moe.moe_grouped_mm_mx4(a, sa, w, sw, offsets_of(counts))
+    for lo, e in ((0, 0), (29_999, 0), (30_000, 1), (30_002, 1), (30_003, 2), (65_530, 2), (R - 1, 2)):
+        rows = ref.decode(a[lo:lo + 1], sa[lo:lo + 1], "e4m3")
+        want, tol = ref.grouped_mm(rows, w[e:e + 1], sw[e:e + 1], offsets_of([1]))
+        ref.assert_within(y[lo:lo + 1], want, tol, f"row {lo}")
+
+
+def test_grouped_mm_weights_past_2_to_31_bytes():
+    E, N, K = 300, 32_768, 512
+    w = torch.randint(0, 256, (E, N, K // 2), generator=gen(64), device="cuda", dtype=U8)
+    sw = torch.randint(120, 130, (E, N, K // 32), generator=gen(65), device="cuda", dtype=U8)
+    a, sa = moe.moe_quantize_mx(randn(6, K, g=gen(66)).to(BF16), "e4m3")
+    counts = [0] * E
+    counts[1], counts[-2], counts[-1] = 2, 1, 3
+    y = moe.moe_grouped_mm_mx4(a, sa, w, sw, offsets_of(counts))
+    rows = ref.decode(a, sa, "e4m3")
+    for lo, hi, e in ((0, 2, 1), (2, 3, E - 2), (3, 6, E - 1)):
+        want, tol = ref.grouped_mm(rows[lo:hi], w[e:e + 1], sw[e:e + 1], offsets_of([hi - lo]))
+        ref.assert_within(y[lo:hi], want, tol, f"expert {e}")
+
+
 # ------------------------------------------------------------------ the FFN and the layer
 
 
