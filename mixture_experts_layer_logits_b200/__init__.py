@@ -336,7 +336,7 @@ def _out(t, name, like, dtype, shape):
     """The given output tensor, checked, or a new one on the device of `like`."""
     if t is None:
         return like.new_empty(shape, dtype=dtype)
-    _same(t, name, dtype, torch.Size(shape), like.device)
+    _same(t, name, dtype, shape, like.device)
     return t
 
 
@@ -399,7 +399,7 @@ def moe_add_rmsnorm(x, weight, eps: float = 1e-6, residual=None, quantize: bool 
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_add_rmsnorm")
     bf16 = torch.bfloat16
     px = _same(x, "x", bf16, shape, dev)
-    pw = _same(weight, "weight", bf16, torch.Size((H,)), dev)
+    pw = _same(weight, "weight", bf16, (H,), dev)
     pr = ps = pc = psc = None
     if residual is not None:
         pr = _same(residual, "residual", bf16, shape, dev)
@@ -440,15 +440,15 @@ def moe_grouped_mm_mx4(a, a_scale, w, w_scale, expert_offsets, ws=None, y=None):
                          f"{tuple(w.shape)}")
     R, K = a.shape
     E, N, _ = w.shape
-    dev, u8, size = a.device, torch.uint8, torch.Size
+    dev, u8 = a.device, torch.uint8
     shape, need = _mm_plan(R, E, N, K)
     if need == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_grouped_mm_mx4")
-    ptrs = (_same(a, "a", u8, size((R, K)), dev),
-            _same(a_scale, "a_scale", u8, size((R, K // 32)), dev),
-            _same(w, "w", u8, size((E, N, K // 2)), dev),
-            _same(w_scale, "w_scale", u8, size((E, N, K // 32)), dev),
-            _same(expert_offsets, "expert_offsets", torch.int32, size((E + 1,)), dev))
+    ptrs = (_same(a, "a", u8, (R, K), dev),
+            _same(a_scale, "a_scale", u8, (R, K // 32), dev),
+            _same(w, "w", u8, (E, N, K // 2), dev),
+            _same(w_scale, "w_scale", u8, (E, N, K // 32), dev),
+            _same(expert_offsets, "expert_offsets", torch.int32, (E + 1,), dev))
     y = _out(y, "y", a, torch.bfloat16, (R, N))
     ws = _workspace_of(ws, need, a)
     _call(load_library().moe_grouped_mm_mx4, "moe_grouped_mm_mx4", dev, *ptrs, shape,
@@ -494,14 +494,14 @@ def _mx4_operands(where, x, x_scale, w13, w13_scale, w2, w2_scale, top_k):
     shape, need = _mx4_plan(T, E, top_k, H, I)
     if need == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, where)
-    dev, u8, size = x.device, torch.uint8, torch.Size
+    dev, u8 = x.device, torch.uint8
     return shape, need, (
-        _same(x, "x", u8, size((T, H)), dev),
-        _same(x_scale, "x_scale", u8, size((T, H // 32)), dev),
-        _same(w13, "w13", u8, size((E, 2 * I, H // 2)), dev),
-        _same(w13_scale, "w13_scale", u8, size((E, 2 * I, H // 32)), dev),
-        _same(w2, "w2", u8, size((E, H, I // 2)), dev),
-        _same(w2_scale, "w2_scale", u8, size((E, H, I // 32)), dev))
+        _same(x, "x", u8, (T, H), dev),
+        _same(x_scale, "x_scale", u8, (T, H // 32), dev),
+        _same(w13, "w13", u8, (E, 2 * I, H // 2), dev),
+        _same(w13_scale, "w13_scale", u8, (E, 2 * I, H // 32), dev),
+        _same(w2, "w2", u8, (E, H, I // 2), dev),
+        _same(w2_scale, "w2_scale", u8, (E, H, I // 32), dev))
 
 
 def moe_grouped_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, expert_offsets, permuted_rows,
@@ -512,8 +512,8 @@ def moe_grouped_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, expert_offsets
     shape, need, ptrs = _mx4_operands("moe_grouped_ffn_mx4", x, x_scale, w13, w13_scale, w2,
                                       w2_scale, top_k)
     dev, R = x.device, shape.T * top_k
-    off = _same(expert_offsets, "expert_offsets", torch.int32, torch.Size((shape.E + 1,)), dev)
-    rows = _same(permuted_rows, "permuted_rows", torch.int32, torch.Size((R,)), dev)
+    off = _same(expert_offsets, "expert_offsets", torch.int32, (shape.E + 1,), dev)
+    rows = _same(permuted_rows, "permuted_rows", torch.int32, (R,), dev)
     y = _out(y, "y", x, torch.bfloat16, (R, shape.H))
     ws = _workspace_of(ws, need, x)
     _call(load_library().moe_grouped_ffn_mx4, "moe_grouped_ffn_mx4", dev, *ptrs, off, rows, shape,
@@ -529,8 +529,8 @@ def moe_forward_mx4(x, x_scale, logits, w13, w13_scale, w2, w2_scale, top_k: int
     shape, need, ptrs = _mx4_operands("moe_forward_mx4", x, x_scale, w13, w13_scale, w2, w2_scale,
                                       top_k)
     dev, T, E = x.device, shape.T, shape.E
-    plog = _same(logits, "logits", torch.float32, torch.Size((T, E)), dev)
-    extra = [None if t is None else _same(t, name, dt, torch.Size(shp), dev)
+    plog = _same(logits, "logits", torch.float32, (T, E), dev)
+    extra = [None if t is None else _same(t, name, dt, shp, dev)
              for t, name, dt, shp in ((topk_ids, "topk_ids", torch.int32, (T, top_k)),
                                       (topk_weights, "topk_weights", torch.float32, (T, top_k)),
                                       (expert_offsets, "expert_offsets", torch.int32, (E + 1,)),

@@ -1,11 +1,9 @@
-// mx_gemm.cuh -- pieces shared by the two kernels of the microscaled grouped products
-// (mx_pair.cu: many rows per expert; mx_stream.cu: few): block-scaled MMA wrappers, the
-// tiles of the groups, and the scale loaders.
+// mx_gemm.cuh -- building blocks of the microscaled grouped products (mx_grouped.cu): block-scaled
+// MMA wrappers, the tiles of the groups, the scale loader, tensor maps and the launch.
 //
-//   D[m, n] = sum_b 2^(sa[m, b] + sb[n, b] - 254) sum_{i in block b} a[m, i] b[n, i]
+//   D[f, j] = sum_b 2^(sw[f, b] + sa[j, b] - 254) sum_{i in block b} w[f, i] a[j, i]
 //
-// with E2M1 weights and E4M3 tokens (one of them a, the other b), blocks of 32 and E8M0
-// scales.  Products of codes and their power-of-two scales are exact, so only the fp32
+// with E2M1 weights w, E4M3 token rows a, blocks of 32 and E8M0 scales.  Products of codes and their power-of-two scales are exact, so only the fp32
 // sums round.
 //
 // Weights lie in shared memory one byte an element: TMA unpacks the 4-bit codes to the
@@ -33,11 +31,7 @@ namespace mx {
 
 constexpr int kBK = 128;                    // K elements per stage: one 128-byte swizzle row
 constexpr int kMaxExperts = 1024;
-// weight rows of one TMA box (MODE 0 loads gate and up rows of 32 features in turn)
-template <int MODE>
-constexpr int kWBox = MODE == 0 ? 32 : 64;
 constexpr int kRowTx = kBK / 2;             // an unpacking TMA load counts its packed bytes
-constexpr int kSfCols = 16;                 // TMEM columns per stage for scales: 4 + 8 used
 constexpr int kTableBytes = 2 * (kMaxExperts + 1) * 4 + 120;
 
 // ------------------------------------------------------------------ PTX
@@ -68,15 +62,11 @@ __device__ __forceinline__ bool warp_agrees(bool ok)
     return ok;
 }
 
-// Instruction descriptor of kind::mxf8f6f4, both operands K-major, E8M0 scales.  Format
-// codes: E4M3 0, E2M1 5.
-__host__ __device__ constexpr uint32_t idesc_formats(bool a_is_weight)
+// Instruction descriptor of kind::mxf8f6f4: E2M1 A (code 5), E4M3 B (code 0), both
+// K-major, E8M0 scales.
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N)
 {
-    return (a_is_weight ? 5u << 7 : 5u << 10) | (1u << 23);
-}
-__device__ __forceinline__ uint32_t idesc_shape(int M, int N)
-{
-    return ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+    return (5u << 7) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24);
 }
 // Its bits that select the scale byte of K block kb, 0..3, for B and A.
 __device__ __forceinline__ constexpr uint32_t idesc_kb(int kb)
@@ -84,27 +74,17 @@ __device__ __forceinline__ constexpr uint32_t idesc_kb(int kb)
     return ((uint32_t)kb << 4) | ((uint32_t)kb << 29);
 }
 
-// CG: CTAs that work on one MMA (cta_group::1 or ::2).
-template <int CG>
-__device__ __forceinline__ void umma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
-                                     uint32_t sfb, uint32_t accumulate)
+// D (+)= A B^T with scales, one MMA of a pair of CTAs (cta_group::2).
+__device__ __forceinline__ void umma_mx(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
-            "[%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
-            "[%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, "
+        "[%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
 }
 
 // Shared-memory descriptor of 512 bytes of scales: 32 rows of 16 bytes, no swizzle,
@@ -115,38 +95,24 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t smem)
            ((uint64_t)1 << 46);
 }
 
-// Copies them to 4 TMEM columns, the same 32 lanes' worth in every lane quarter.
-// Ordered before later MMAs of this thread.  With CG = 2 each of the two CTAs copies from
-// its own shared memory to its own TMEM.
-template <int CG>
+// Copies them to 4 TMEM columns, the same 32 lanes' worth in every lane quarter, ordered
+// before later MMAs of this thread.  Each CTA of the pair copies from its own shared memory to
+// its own TMEM.
 __device__ __forceinline__ void scales_to_tmem(uint32_t taddr, uint64_t desc)
 {
-    if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                     : "memory");
-    else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
-                     : "memory");
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// 2D TMA load of a box at (c, row) into this CTA's shared memory whose bytes count on
-// `bar`.  CG = 2: `bar` may lie in the other CTA of the pair.
-template <int CG>
+// 2D TMA load of a box at (c, row) into this CTA's shared memory, whose bytes count on `bar`,
+// which may lie in the other CTA of the pair.
 __device__ __forceinline__ void tma_2d(uint32_t dst, const void* tmap, uint32_t bar, int c, int row,
                                        uint64_t policy)
 {
-    if constexpr (CG == 1)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
-            : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
-            "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
-            : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2.L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c), "r"(row), "l"(policy)
+        : "memory");
 }
 
 // ------------------------------------------------------------------ groups and tiles
@@ -292,12 +258,11 @@ __device__ __forceinline__ int tile_feature(int r) { return r / 64 * 32 + r % 32
 __device__ __forceinline__ bool tile_row_is_up(int r) { return r / 32 % 2; }
 
 // The kScaleWarps warps that bring scales into the ring.  Reading 4 bytes a row and K tile costs one
-// L1 line lookup and a 32-byte sector each time, so a row is read a group of 8 K tiles at a
-// time (32 bytes; in 16-byte loads where the row pitch allows it) into registers, one group
-// ahead, and stored 4 bytes a stage.  The rows are split over four warps because a stage costs a
-// warp some 200 cycles whatever it stores (the fence towards tcgen05.cp's proxy, the arrival);
-// two teams of two warps that took groups of 4 K tiles in turn, 16 bytes a row, fetched each
-// sector twice: prefill 1.27 ms instead of SCALEFIG.
+// L1 line lookup and a 32-byte sector each time (as cp.async copies that was half of w13's time
+// at T = 8192), so a row is read a group of 8 K tiles at a time (32 bytes; in 16-byte loads
+// where the row pitch allows it) into registers, one group ahead, and stored 4 bytes a stage.
+// The rows are split over four warps: a stage costs a warp some 200 cycles whatever it stores
+// (the fence towards tcgen05.cp's proxy, the arrival), which must stay under its 410.
 //   units       unit0, unit0 + stride, ... below `units`, each of num_kt K tiles
 //   kRows       rows of this thread; put[i]: where row i's bytes go within a stage's scales,
 //               or -1
@@ -398,9 +363,10 @@ inline cudaError_t weights_map(CUtensorMap* m, const void* base, uint64_t rows, 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Launches kern as pairs of CTAs.
 template <auto kern>
-cudaError_t launch(int grid, int cluster, int threads, int smem, cudaStream_t st,
-                   const CUtensorMap& tw, const CUtensorMap& ta, const MxArgs& g)
+cudaError_t launch_pairs(int grid, int threads, int smem, cudaStream_t st, const CUtensorMap& tw,
+                         const CUtensorMap& ta, const MxArgs& g)
 {
     // the attribute stays with the kernel (one `done` per instantiation), so it is set once a device
     static std::atomic<uint64_t> done{0};
@@ -422,10 +388,10 @@ cudaError_t launch(int grid, int cluster, int threads, int smem, cudaStream_t st
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, tw, ta, g);
 }
 

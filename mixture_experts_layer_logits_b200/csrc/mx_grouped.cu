@@ -1,17 +1,27 @@
-// mx_pair.cu -- microscaled grouped products for many token rows per expert: two CTAs of a
-// cluster work on one MMA (cta_group::2, M = 256 weight rows, N up to 208 token rows).
+// mx_grouped.cu -- products grouped by expert of E4M3 token rows with E2M1 weights, both in
+// microscaled blocks, alone and as the two products of the expert FFN, on block-scaled tcgen05
+// tensor cores.
 //
 //   MODE 0  act[p, f] = MX(silu(gate) * up) of x[rows[p] / k] with w13[e] rows f and I + f
 //   MODE 1  y[rows[p] or p, f] = w[e] row f dotted with act (or any E4M3 rows) [p]
 //
-// Weights are the M operand and an expert's token rows the N columns, rounded up to 16 per
-// tile, so a ragged group costs at most 15 padded columns.  A pair of CTAs reads each weight
-// row and each token row once (its half of both per CTA): the single-CTA form with N = 128 was
-// bound by L2 (11.5 TB/s of operand reads) at 2.11 ms for T = 8192, E = 128, k = 8, H = 4096,
-// I = 1536.
+// Two CTAs of a cluster work on one MMA (cta_group::2): its M = 256 rows are weight rows, 128 per
+// CTA, its N columns an expert's token rows, rounded up to 16 per tile, so few tokens cost few
+// columns and a ragged group at most 15 padded ones.  Why this shape (cycles per K tile of 128,
+// i.e. 4 MMAs and the scale copies; an SM streaming 128 packed weight rows of it at its share of
+// HBM takes 380):
+//   - one CTA, M = 128, N = 16: 502; the pair 409 for twice the rows.  An MMA takes 90 cycles or
+//     more to read its M operand, and a scale copy in between costs the pair less.
+//   - token rows as the M operand, N = 256 weight rows: 523 for 256 rows a CTA, so HBM-bound; but an
+//     MMA then multiplies 128 rows however few are tokens, and the power that takes lowers the
+//     clock: T = 64, E = 256, skewed, H = 7168, I = 2048 took 136 us under sustained load (114 in
+//     a burst), the pair 112 (99).
+//   - many tokens: a pair reads each weight row and each token row once, half of both per CTA.
+//     One CTA with N = 128 was bound by its reads from L2 (T = 8192, E = 128, k = 8, H = 4096,
+//     I = 1536: 2.11 ms, the pair 1.2 in a burst and 1.37 under the power cap of sustained load).
 //
-// Warp roles: 0 TMA; 1 TMEM, and in CTA 0 MMA issue for both; 2-3 and 12-13
-// scales; 4-11 epilogue; MODE 0: 14-15 gather of token rows.
+// Warp roles: 0 TMA; 1 TMEM, and in CTA 0 MMA issue for both; 2-3 and 12-13 scales; 4-11
+// epilogue; MODE 0: 14-15 gather of token rows.
 //   - MODE 1 loads token rows by TMA with the weights; MODE 0 gathers x rows with 16-byte
 //     cp.async copies straight to their swizzled places.  (26 gather4 TMA loads a stage, one
 //     per lane, issue too slowly: w13 took 1.70 ms instead of 0.97.)
@@ -168,7 +178,7 @@ __device__ __forceinline__ void store_matrix_x4_trans(uint32_t addr, uint32_t a,
 
 template <int MODE, int NT>
 __global__ void __launch_bounds__(kThreads, 1)
-    mx_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
+    mx_grouped_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_a,
                    const MxArgs g)
 {
     using C = Cfg<MODE, NT>;
@@ -269,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (rank == 0) mbar_arrive_expect_tx(&aux->full[stage], bytes);
 #pragma unroll
                     for (int r = 0; r < kBM; r += kWBoxRows<MODE>)
-                        tma_2d<2>(st + r * kBK, &tm_w, bar, kt * kBK,
+                        tma_2d(st + r * kBK, &tm_w, bar, kt * kBK,
                                   row + (MODE == 0 ? tile_feature(r) + (tile_row_is_up(r) ? g.N : 0) : r), wpol);
                 }
                 if (MODE == 1) {
@@ -278,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         dep = true;
                     }
                     __syncwarp();
-                    if (elect_one()) tma_2d<2>(st + kATile, &tm_a, bar, kt * kBK, trow, tpol);
+                    if (elect_one()) tma_2d(st + kATile, &tm_a, bar, kt * kBK, trow, tpol);
                 }
                 __syncwarp();
                 ++fills;
@@ -338,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const int n = padded(t.rows);
             const uint32_t d = tmem_base + (uint32_t)(b * NT);
-            const uint32_t idesc = idesc_formats(true) | idesc_shape(2 * kBM, n);
+            const uint32_t idesc = idesc_mx(2 * kBM, n);
             for (int kt = 0; kt < num_kt; ++kt) {
                 ok = warp_agrees((MODE == 1 || mbar_wait(&aux->gathered[stage], phase, abort_flag)) &&
                                  mbar_wait_cluster(&aux->full[stage], phase, abort_flag));
@@ -351,12 +361,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t ds = scale_desc(sf);
                 if (elect_one()) {
                     if (MODE == 0) fence_proxy_async_smem();  // this CTA's rows came by cp.async
-                    scales_to_tmem<2>(tsf, ds);
-                    scales_to_tmem<2>(tsf + 4, ds + (512 >> 4));
-                    if (NT > 128 && n > 128) scales_to_tmem<2>(tsf + 8, ds + (1024 >> 4));
+                    scales_to_tmem(tsf, ds);
+                    scales_to_tmem(tsf + 4, ds + (512 >> 4));
+                    if (NT > 128 && n > 128) scales_to_tmem(tsf + 8, ds + (1024 >> 4));
 #pragma unroll
                     for (int kk = 0; kk < kBK / 32; ++kk)  // 32 bytes along K
-                        umma<2>(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
+                        umma_mx(d, da + 2 * kk, db + 2 * kk, idesc | idesc_kb(kk), tsf, tsf + 4,
                                 (kt | kk) ? 1u : 0u);
                     commit(&aux->empty[stage]);
                     if (kt + 1 == num_kt) commit(&aux->tfull[b]);
@@ -672,16 +682,20 @@ cudaError_t launch_nt(MxArgs g, cudaStream_t st)
         e = MODE == 1 ? gemm::make_tmap_u8(&ta, g.a, (uint64_t)g.R, (uint64_t)g.K, C::kBRows, kBK)
                       : (ta = tw, e);
     if (e != cudaSuccess) return e;
-    return launch<mx_pair_kernel<MODE, NT>>(device_sms() / 2 * 2, 2, kThreads, C::kSmem, st, tw, ta, g);
+    return launch_pairs<mx_grouped_kernel<MODE, NT>>(device_sms() / 2 * 2, kThreads, C::kSmem, st, tw, ta, g);
 }
 
+// Token rows per tile.  A tile that holds all of an expert's rows reads its weights once, and a
+// wider tile than needed costs little (E = 32, N = K = 2048, 2 rows an expert: NT = 16 16.0 us,
+// 64 16.5, 128 16.7); beyond 64 the average decides: 64 rows an expert 128 19.2 us, 208 21.8; 128
+// rows 22.1 and 24.5; 160 rows 30.8 and 26.5; 400 rows 62.5 and 49.8.
 template <int MODE>
 cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
 {
     if (most <= 16) return launch_nt<MODE, 16>(g, st);
     if (most <= 32) return launch_nt<MODE, 32>(g, st);
     if (most <= 64) return launch_nt<MODE, 64>(g, st);
-    if (g.R < 64LL * g.E) return launch_nt<MODE, 128>(g, st);
+    if (g.R <= 128LL * g.E) return launch_nt<MODE, 128>(g, st);
     return launch_nt<MODE, 208>(g, st);
 }
 
