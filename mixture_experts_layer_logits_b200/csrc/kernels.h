@@ -1,5 +1,5 @@
 // kernels.h -- host-side launch interface between the C ABI (moe_api.cu) and the
-// kernels (route_permute.cu, grouped_ffn.cu, combine.cu).  Internal only.
+// kernels (route_permute.cu, grouped_ffn.cu, combine.cu, mx_quant.cu, mx_grouped.cu).  Internal only.
 #pragma once
 
 #include <cuda.h>

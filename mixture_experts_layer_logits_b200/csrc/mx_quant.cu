@@ -38,7 +38,8 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&v)[8])
 // A matrix whose columns are a multiple of 32 is a run of blocks, whatever its rows:
 // four consecutive threads hold one block, 8 elements each.  HBM-bound; a thread has U
 // chunks' loads in flight before it uses the first (201 M bf16 elements to E2M1: U = 1
-// 104 us, 2 86 us, 4 78.5 us, which is the measured copy rate, 8 80 us).
+// 104 us, 2 86 us, 4 78.5 us, which is the measured copy rate, 8 80 us).  An fp32 chunk is two
+// loads and needs no more (134 M elements to E4M3: U = 1 98.9 us, the measured copy rate, 2 100.8).
 template <bool E2M1, typename Src, int U>
 __global__ void __launch_bounds__(256)
     quantize_kernel(const Src* __restrict__ src, long chunks, uint8_t* __restrict__ codes,
@@ -159,9 +160,11 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st)
 {
     const int chunks = a.H / 8;
     // Chunks of 8 elements: one per thread where there are few rows, and CTAs of 256 threads
-    // where rows fill the SMs (8192 x 4096 with residual and blocks: 48.5 us, 97% of the measured
-    // copy rate; with CTAs of 512 54.6 us, of 128 53.1 us).
-    const int most = a.T >= 4 * device_sms() ? 256 : 1024;
+    // where rows fill the SMs several times (8192 x 4096 with residual and blocks: 48.5 us, 97% of
+    // the measured copy rate; with CTAs of 512 54.6 us, of 128 53.1 us).  CTAs of up to 1024 and of
+    // 256 threads at H = 7168: 64 rows 2.6 and 4.0 us, 592 7.0 and 9.7, 888 10.9 and 12.0, 1036
+    // 13.4 and 12.8, 4096 48.5 and 42.2; at H = 4096 they cross between 888 and 1036 rows too.
+    const int most = a.T >= 7 * device_sms() ? 256 : 1024;
     const int c = (chunks + most - 1) / most;
     const int cc = c <= 1 ? 1 : c <= 2 ? 2 : c <= 4 ? 4 : 8;
     const int threads = ((chunks + cc - 1) / cc + 31) & ~31;
@@ -191,11 +194,10 @@ cudaError_t launch_quantize_mx(const void* src, bool f32, long n, bool e2m1, uin
                                uint8_t* scales, cudaStream_t st)
 {
     const long chunks = n / 8;
-    // A grid that does not fill the SMs gains nothing from longer threads.
-    const bool many = chunks > 2048L * 4 * device_sms();
-    if (f32)
-        return many ? launch_quantize<float, 2>(src, chunks, e2m1, codes, scales, st)
-                    : launch_quantize<float, 1>(src, chunks, e2m1, codes, scales, st);
+    // Several chunks a thread pay once the grid fills the SMs for all that (bf16 to E4M3, U = 1 and
+    // 4: 2.1 M elements 1.8 and 3.0 us, 5.2 M 3.8 and 3.8, 8.4 M 5.6 and 5.1, 134 M 73.7 and 60.6).
+    const bool many = chunks > 4096L * device_sms();
+    if (f32) return launch_quantize<float, 1>(src, chunks, e2m1, codes, scales, st);
     return many ? launch_quantize<uint16_t, 4>(src, chunks, e2m1, codes, scales, st)
                 : launch_quantize<uint16_t, 1>(src, chunks, e2m1, codes, scales, st);
 }

@@ -55,6 +55,12 @@ def test_quantize_is_exact(shape, dtype, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_many_blocks_ragged_end(dtype, fmt):
+    check_quantised(randn(5003, 1056, g=gen(1)).to(dtype), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 def test_quantize_every_bf16_value(fmt):
     """Every finite bf16 value beside a largest magnitude of each binade: all ties, saturation,
     subnormal elements and scales, both zeros."""
@@ -121,6 +127,11 @@ def test_norm(T, H, residual):
     assert got2 is out2 and none is None and none2 is None and torch.equal(out2, out)
     if residual:
         assert h2 is res and torch.equal(res, h)
+
+
+@pytest.mark.parametrize("T,H", [(1035, 4128), (1100, 2080), (1100, 6176), (1100, 8224), (1100, 16416)])
+def test_norm_many_rows(T, H):
+    test_norm(T, H, True)
 
 
 def test_norm_extremes():
