@@ -53,11 +53,9 @@ constexpr int kWBoxRows = MODE == 0 ? 32 : kBM;
 constexpr int kEpiWarp0 = 4, kEpiWarps = 8, kGatherWarp0 = 14, kGatherWarps = 2;
 constexpr int kThreads = 32 * (kGatherWarp0 + kGatherWarps);  // whole warpgroups; MODE 1 leaves two warps idle
 constexpr int kMaxStages = 12;
-// epilogue shared memory per warp: MODE 0, 2 buffers of 8 columns x 32 lanes of fp32 to swap, and 2
-// of 8 token rows of 32 E4M3 codes (48 bytes apart: the rows that a store hits share no bank);
-// MODE 1, 2 buffers of 8 token rows x 32 bf16
-constexpr int kCodePitch = 48;
-constexpr int kWarpStaging = 2 * 1024 + 2 * 8 * kCodePitch;
+// epilogue shared memory per warp: MODE 0, 2 buffers of 8 columns x 32 lanes of fp32 to swap; MODE 1,
+// 2 buffers of 8 token rows x 32 bf16
+constexpr int kWarpStaging = 2 * 1024;
 
 // NT: the most token rows of a tile.
 template <int MODE, int NT>
@@ -174,6 +172,39 @@ __device__ __forceinline__ void store_matrix_x4_trans(uint32_t addr, uint32_t a,
     asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
                  "r"(a), "r"(b), "r"(c), "r"(d)
                  : "memory");
+}
+
+// silu(g) u = g u / (1 + 2^(-g log2 e)).  Exponential and reciprocal are one instruction each, a few
+// ulp of fp32, far inside the rounding to E4M3; where the power overflows the reciprocal is 0.
+__device__ __forceinline__ float swiglu(float g, float u)
+{
+    float p, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + p));
+    return g * r * u;
+}
+
+// The largest magnitude of four, NaN if one of them is.
+__device__ __forceinline__ float max_abs4(float a, float b, float c, float d)
+{
+    float m;
+    asm("{\n\t.reg .f32 t;\n\t"
+        "max.NaN.f32 t, %1, %2;\n\t"
+        "max.NaN.f32 %0, %3, %4;\n\t"
+        "max.NaN.f32 %0, %0, t;\n\t}"
+        : "=&f"(m)
+        : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)), "f"(fabsf(d)));
+    return m;
+}
+
+// 4 x 4 bytes transposed over the lanes whose l differs in its lower 2 bits (lanes 4 apart): byte i
+// of the lane with l % 4 = b goes to byte b of the one with l % 4 = i.
+__device__ __forceinline__ uint32_t transpose_bytes(uint32_t q, int l)
+{
+    uint32_t o = __shfl_xor_sync(0xffffffffu, q, 4);
+    q = __byte_perm(q, o, l & 1 ? 0x3715 : 0x6240);
+    o = __shfl_xor_sync(0xffffffffu, q, 8);
+    return __byte_perm(q, o, l & 2 ? 0x3276 : 0x5410);
 }
 
 template <int MODE, int NT>
@@ -532,82 +563,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // warps 1 and 3 their ups.  Of every two column blocks the gate warp finishes the
                 // first and the up warp the second: they swap the other halves through shared
                 // memory.  A lane then has features lane / 4 + 0, 8, 16, 24 of tokens 2 (lane % 4)
-                // and the next; codes leave as 32-byte rows.
+                // and the next.
                 const int up = lq & 1;
                 uint8_t* const ex = staging + (warp - kEpiWarp0) * kWarpStaging;
                 const uint8_t* const other = staging + ((warp ^ 1) - kEpiWarp0) * kWarpStaging;
-                uint8_t* const codes = ex + 2 * 1024;
                 const int f = first_feature(t) + (lq >> 1) * 32;
-                int step = 0;
-                for (int c = 0; c < kBlocks && jbeg + c * 8 < jend; c += 2, ++step) {
-                    const bool two = c + 1 < kBlocks;
-                    uint32_t v[2][8];
-                    tmem_ld_16x256(acc + jbeg + c * 8, v[0]);
-                    tmem_ld_16x256(acc + (16u << 16) + jbeg + c * 8, v[0] + 4);
-                    if (two) {
-                        tmem_ld_16x256(acc + jbeg + c * 8 + 8, v[1]);
-                        tmem_ld_16x256(acc + (16u << 16) + jbeg + c * 8 + 8, v[1] + 4);
-                    }
+                for (int c = 0; c < kBlocks && jbeg + c * 8 < jend; c += 2) {
+                    // (past the last block the loads only keep the warps alike)
+                    const int cb = c + up;                    // the block that this warp finishes
+                    const int cg = min(c + 1 - up, kBlocks - 1);  // the one that it gives away
+                    const uint32_t mine = acc + jbeg + min(cb, kBlocks - 1) * 8, give = acc + jbeg + cg * 8;
+                    uint32_t own[8], gift[8];
+                    tmem_ld_16x256(give, gift);
+                    tmem_ld_16x256(give + (16u << 16), gift + 4);
+                    tmem_ld_16x256(mine, own);
+                    tmem_ld_16x256(mine + (16u << 16), own + 4);
                     tmem_ld_wait();
-                    const int buf = (step & 1) * 1024;
-                    uint32_t own[8], give[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        own[i] = up ? v[1][i] : v[0][i];
-                        give[i] = up ? v[0][i] : v[1][i];
-                    }
-                    reinterpret_cast<uint4*>(ex + buf)[lane] = make_uint4(give[0], give[1], give[2], give[3]);
-                    reinterpret_cast<uint4*>(ex + buf)[32 + lane] = make_uint4(give[4], give[5], give[6], give[7]);
+                    const int buf = (c & 2) * 512;
+                    reinterpret_cast<uint4*>(ex + buf)[lane] = make_uint4(gift[0], gift[1], gift[2], gift[3]);
+                    reinterpret_cast<uint4*>(ex + buf)[32 + lane] = make_uint4(gift[4], gift[5], gift[6], gift[7]);
                     named_bar_sync(3 + grp * 2 + (lq >> 1), 64);
                     const uint4 o0 = reinterpret_cast<const uint4*>(other + buf)[lane];
                     const uint4 o1 = reinterpret_cast<const uint4*>(other + buf)[32 + lane];
                     const uint32_t got8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-                    const int cb = c + up;  // the block that this warp finishes
                     if (cb >= kBlocks || jbeg + cb * 8 >= jend) continue;  // warp-uniform
                     float a[8];  // even: the first token
-                    uint32_t m0 = 0, m1 = 0;
+                    if (up) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float x = __uint_as_float(own[i]), z = __uint_as_float(got8[i]);
-                        a[i] = up ? silu_mul(z, x) : silu_mul(x, z);
-                        const uint32_t bits = __float_as_uint(a[i]) & 0x7FFFFFFFu;
-                        if (i & 1)
-                            m1 = max(m1, bits);
-                        else
-                            m0 = max(m0, bits);
-                    }
+                        for (int i = 0; i < 8; ++i)
+                            a[i] = swiglu(__uint_as_float(got8[i]), __uint_as_float(own[i]));
+                    } else {
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) {
-                        m0 = max(m0, __shfl_xor_sync(0xffffffffu, m0, o));
-                        m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, o));
+                        for (int i = 0; i < 8; ++i)
+                            a[i] = swiglu(__uint_as_float(own[i]), __uint_as_float(got8[i]));
                     }
-                    const uint32_t s0 = scale_code(m0, kEmaxE4M3), s1 = scale_code(m1, kEmaxE4M3);
+                    // the largest magnitude's exponent is all that the scale takes: the upper halves
+                    // of both tokens' maxima go through the reduction as one register
+                    const uint32_t m0 = __float_as_uint(max_abs4(a[0], a[2], a[4], a[6]));
+                    const uint32_t m1 = __float_as_uint(max_abs4(a[1], a[3], a[5], a[7]));
+                    uint32_t m = __byte_perm(m0, m1, 0x7632);
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    const uint32_t s0 = scale_code(m << 16, kEmaxE4M3), s1 = scale_code(m & 0xFFFF0000u, kEmaxE4M3);
                     const float i0 = inverse_scale(min(s0, 254u)), i1 = inverse_scale(min(s1, 254u));
                     uint32_t q0 = e4m3x4(a[0] * i0, a[2] * i0, a[4] * i0, a[6] * i0);
                     uint32_t q1 = e4m3x4(a[1] * i1, a[3] * i1, a[5] * i1, a[7] * i1);
                     if (s0 == kNanScale) q0 = 0x7F7F7F7Fu;
                     if (s1 == kNanScale) q1 = 0x7F7F7F7Fu;
-                    // 8 tokens x 32 codes, rows kCodePitch apart
-                    uint8_t* const put = codes + (step & 1) * (8 * kCodePitch) + (lane & 3) * (2 * kCodePitch) + (lane >> 2);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        put[i * 8] = (uint8_t)(q0 >> (8 * i));
-                        put[kCodePitch + i * 8] = (uint8_t)(q1 >> (8 * i));
-                    }
-                    __syncwarp();
-                    const int p = t.row + jbeg + cb * 8;
-                    if (lane < 16 && jbeg + cb * 8 + (lane >> 1) < jend)
-                        *reinterpret_cast<uint4*>(g.act + (size_t)(p + (lane >> 1)) * g.N + f + (lane & 1) * 16) =
-                            *reinterpret_cast<const uint4*>(codes + (step & 1) * (8 * kCodePitch) +
-                                                            (lane >> 1) * kCodePitch + (lane & 1) * 16);
-                    // lanes 0 .. 3 hold the scales of tokens 2 lane and 2 lane + 1
+                    // Byte i of q0 and q1 is feature lane / 4 + 8 i.  Transposed over the 4 lanes
+                    // whose lane / 4 differs in its lower 2 bits, a lane has 4 consecutive features
+                    // from 8 (lane / 4 % 4) + 4 (lane / 16), and the warp stores whole 32-byte rows.
+                    q0 = transpose_bytes(q0, lane >> 2), q1 = transpose_bytes(q1, lane >> 2);
+                    const int j = jbeg + cb * 8 + (lane & 3) * 2;
+                    uint8_t* const put = g.act + (size_t)(t.row + j) * g.N + f + (lane >> 2 & 3) * 8 + (lane >> 4) * 4;
+                    if (j < jend) *reinterpret_cast<uint32_t*>(put) = q0;
+                    if (j + 1 < jend) *reinterpret_cast<uint32_t*>(put + g.N) = q1;
                     if (lane < 4) {
-                        uint8_t* const sc = g.act_scale + (size_t)(p + lane * 2) * (g.N / 32) + f / 32;
-                        if (jbeg + cb * 8 + lane * 2 < jend) sc[0] = (uint8_t)s0;
-                        if (jbeg + cb * 8 + lane * 2 + 1 < jend) sc[g.N / 32] = (uint8_t)s1;
+                        uint8_t* const sc = g.act_scale + (size_t)(t.row + j) * (g.N / 32) + f / 32;
+                        if (j < jend) sc[0] = (uint8_t)s0;
+                        if (j + 1 < jend) sc[g.N / 32] = (uint8_t)s1;
                     }
-                    __syncwarp();
                 }
+                __syncwarp();
                 release(b);
             } else {
                 // Drain this group's columns into registers as packed bf16 and hand them back,
