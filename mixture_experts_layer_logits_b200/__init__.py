@@ -335,7 +335,7 @@ def _same(t: torch.Tensor, name: str, dtype, shape, device):
 def _out(t, name, like, dtype, shape):
     """The given output tensor, checked, or a new one on the device of `like`."""
     if t is None:
-        return like.new_empty(shape, dtype=dtype)
+        return like.new_empty(*shape, dtype=dtype)
     _same(t, name, dtype, shape, like.device)
     return t
 
@@ -353,7 +353,7 @@ def _call(fn, where, device, *args):
     if device.type != "cuda":
         raise ValueError(f"{where}: expected CUDA tensors, got {device}")
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(index):
