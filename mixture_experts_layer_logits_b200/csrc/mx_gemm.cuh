@@ -137,40 +137,62 @@ struct Groups {
     const int* first;  // [E + 1] tiles before each expert
     const int* start;  // [E + 1] rows before each expert
     int E;
+};
 
-    // Unit u of tiles x fbs: experts in order; within one, feature block major and tile
-    // minor, so the tiles that share a weight block run at the same time on neighbouring
-    // CTAs and share it in L2.  A group of c rows in t tiles is cut evenly (to 16 rows).
-    // All 32 lanes take part; `e` is the expert of this warp's unit before (a CTA's units
-    // ascend, so the search starts there, 32 experts at a time).
-    __device__ __forceinline__ Unit unit(int u, int fbs, uint32_t fb_magic, int& e) const
+// The units u0, u0 + stride, ... of tiles x fbs, one after the other: experts in order; within one,
+// feature block major and tile minor, so the tiles that share a weight block run at the same time
+// on neighbouring CTAs and share it in L2.  A group of c rows in t tiles is cut evenly (to 16 rows).
+// The lanes look 32 units up at once and hand them out by shuffles: one look-up is a chain of
+// shared-memory reads and divisions of some 600 cycles, more than a K tile's MMAs take.
+struct Units {
+    Groups g;
+    int fbs, units, stride, u;
+    uint32_t fb_magic;
+    int at;     // 0 .. 31: next lane to hand out
+    Unit mine;
+
+    __device__ __forceinline__ Units(const Groups& groups, int fb_count, uint32_t magic, int u0, int step)
+        : g(groups), fbs(fb_count), units(groups.first[groups.E] * fb_count), stride(step), u(u0), fb_magic(magic),
+          at(32)
     {
-        const int lane = threadIdx.x & 31;
-        const int rest = div_by(u, fbs, fb_magic);
-        for (;;) {  // to the last e with first[e] <= rest
-            const int at = e + 1 + lane;
-            const uint32_t past = __ballot_sync(0xffffffffu, at > E || first[min(at, E)] > rest);
-            if (past) {
-                e += __ffs(past) - 1;
-                break;
-            }
-            e += 32;
+    }
+
+    // All 32 lanes take part.  (Past the last unit: the last one again.)
+    __device__ __forceinline__ Unit next()
+    {
+        if (at == 32) {
+            look_up(min(u + (int)(threadIdx.x & 31) * stride, units - 1));
+            u = min(u + 32 * stride, units - 1);
+            at = 0;
         }
-        const int local = u - first[e] * fbs, count = first[e + 1] - first[e];
-        const int rows = start[e + 1] - start[e];
         Unit t;
-        t.expert = e;
-        t.fb = local;
-        t.row = start[e];
-        t.rows = rows;
+        t.expert = __shfl_sync(0xffffffffu, mine.expert, at);
+        t.fb = __shfl_sync(0xffffffffu, mine.fb, at);
+        t.row = __shfl_sync(0xffffffffu, mine.row, at);
+        t.rows = __shfl_sync(0xffffffffu, mine.rows, at);
+        ++at;
+        return t;
+    }
+
+    __device__ __forceinline__ void look_up(int v)
+    {
+        const int rest = div_by(v, fbs, fb_magic);
+        int e = 0;  // to the last e with first[e] <= rest
+        for (int step = 1 << (31 - __clz(g.E)); step; step >>= 1)
+            if (e + step < g.E && g.first[e + step] <= rest) e += step;
+        const int local = v - g.first[e] * fbs, count = g.first[e + 1] - g.first[e];
+        const int rows = g.start[e + 1] - g.start[e];
+        mine.expert = e;
+        mine.fb = local;
+        mine.row = g.start[e];
+        mine.rows = rows;
         if (count > 1) {
             const int per = ((rows + count - 1) / count + 15) & ~15;
-            t.fb = local / count;
-            const int at = (local - t.fb * count) * per;
-            t.row += at;
-            t.rows = min(per, rows - at);
+            mine.fb = local / count;
+            const int from = (local - mine.fb * count) * per;
+            mine.row += from;
+            mine.rows = min(per, rows - from);
         }
-        return t;
     }
 };
 

@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int fbs = g.fb_count;
     const int units = groups.first[g.E] * fbs;
     const int num_kt = g.K / kBK;
-    auto unit = [&](int u, int& e) { return groups.unit(u, fbs, g.fb_magic, e); };
+    Units list(groups, fbs, g.fb_magic, unit0, stride);
     auto padded = [](int rows) { return (rows + 15) & ~15; };  // the MMA's N
     // this CTA's part of a unit: its first output feature, and its first token row in the tile.
     // MODE 1: the second CTA's features may begin past N; it then works on the first ones
@@ -297,11 +297,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ring0 = smem_u32(ring);
         const uint32_t bytes = 2 * (kBM * kRowTx + (MODE == 1 ? kBTile : 0));
         const uint32_t full0 = in_leader(&aux->full[0]);
-        int stage = 0, fills = 0, e = 0;
+        int stage = 0, fills = 0;
         uint32_t phase = 0;
         bool ok = true, dep = !(MODE == 1 && g.early);
         for (int u = unit0; u < units && ok; u += stride) {
-            const Unit t = unit(u, e);
+            const Unit t = list.next();
             const int f = first_feature(t);
             const int row = MODE == 0 ? t.expert * 2 * g.N + f : t.expert * g.N + (f < g.N ? f : 0);
             const int trow = t.row + first_token(t);
@@ -370,12 +370,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        int stage = 0, lu = 0, e = 0;
+        int stage = 0, lu = 0;
         uint32_t phase = 0;
         bool ok = true;
         const uint32_t ring0 = smem_u32(ring);
         for (int u = unit0; u < units && ok; u += stride, ++lu) {
-            const Unit t = unit(u, e);
+            const Unit t = list.next();
             const int b = lu % kNBuf;
             ok = warp_agrees(
                 mbar_wait_cluster(&aux->tempty[b], (uint32_t)((lu / kNBuf) & 1) ^ 1u, abort_flag));
@@ -432,10 +432,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kTok; ++i)
             put[1 + i] = i0 + i * 128 < NT ? (int)(512 + scale_place(i0 + i * 128)) : -1;
-        int e = 0, tok[kTok];
+        int tok[kTok];
         Unit next;
         auto fetch = [&](int u) {
-            next = unit(u, e);
+            next = list.next();
 #pragma unroll
             for (int i = 0; i < kTok; ++i) {
                 // past the tile's end any scale will do
@@ -477,12 +477,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // other CTA's); CTA 0's MMA warp waits for that, CTA 1's warp 1 relays it.
         const int i0 = threadIdx.x - kGatherWarp0 * 32;
         const uint64_t pol = l2_policy_evict_last();
-        int q = 0, e = 0;
+        int q = 0;
         bool ok = true;
         int r[C::kGIters];
         auto next_rows = [&](int u) {
             if (u >= units) return;
-            const Unit t = unit(u, e);
+            const Unit t = list.next();
 #pragma unroll
             for (int i = 0; i < C::kGIters; ++i) {
                 const int j = (i0 + i * kGatherWarps * 32) >> 3;
@@ -534,9 +534,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_leader(&aux->tempty[b]);
         };
-        int lu = 0, e = 0;
+        int lu = 0;
         for (int u = unit0; u < units; u += stride, ++lu) {
-            const Unit t = unit(u, e);
+            const Unit t = list.next();
             const int b = lu % kNBuf;
             const int jend = min(t.rows, jbeg + kGroupCols);
             // MODE 1: lane i holds the y rows of the group's columns i, i + 32, ...
