@@ -15,10 +15,10 @@
 //   - token rows as the M operand, N = 256 weight rows: 523 for 256 rows a CTA, so HBM-bound; but an
 //     MMA then multiplies 128 rows however few are tokens, and the power that takes lowers the
 //     clock: T = 64, E = 256, skewed, H = 7168, I = 2048 took 136 us under sustained load (114 in
-//     a burst), the pair 112 (99).
+//     a burst), the pair 108 (94).
 //   - many tokens: a pair reads each weight row and each token row once, half of both per CTA.
 //     One CTA with N = 128 was bound by its reads from L2 (T = 8192, E = 128, k = 8, H = 4096,
-//     I = 1536: 2.11 ms, the pair 1.2 in a burst and 1.37 under the power cap of sustained load).
+//     I = 1536: 2.11 ms, the pair 1.2 in a burst and 1.34 under the power cap of sustained load).
 //
 // Warp roles: 0 TMA; 1 TMEM, and in CTA 0 MMA issue for both; 2-3 and 12-13 scales; 4-11
 // epilogue; MODE 0: 14-15 gather of token rows.
@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == 0) {
         // ------------------------------------------------------------ TMA producer
-        // Weights that one tile reads once leave L2 first (T = 8, E = 128: 12.2 us for the down
-        // product, 12.5 without); where several tiles share them they stay (T = 8192: 375 us, 391
-        // with evict_first).  Token rows are read again per feature block (12.2 us; 15.7 with the
+        // Weights that one tile reads once leave L2 first (T = 8, E = 128: 11.8 us for the down
+        // product, 12.1 without); where several tiles share them they stay (T = 8192: 384 us, 391
+        // with evict_first).  Token rows are read again per feature block (11.8 us; 16.0 with the
         // default policy).
         const uint64_t wpol = g.stream_weights ? l2_policy_evict_first() : l2_policy_evict_normal();
         const uint64_t tpol = l2_policy_evict_last();
@@ -713,9 +713,9 @@ cudaError_t launch_nt(MxArgs g, cudaStream_t st)
 }
 
 // Token rows per tile.  A tile that holds all of an expert's rows reads its weights once, and a
-// wider tile than needed costs little (E = 32, N = K = 2048, 2 rows an expert: NT = 16 16.0 us,
-// 64 16.5, 128 16.7); beyond 64 the average decides: 64 rows an expert 128 19.2 us, 208 21.8; 128
-// rows 22.1 and 24.5; 160 rows 30.8 and 26.5; 400 rows 62.5 and 49.8.
+// wider tile than needed costs little (E = 32, N = K = 2048, 2 rows an expert: NT = 16 15.9 us,
+// 64 16.1, 128 16.3, 208 18.5); beyond 64 the average decides: 64 rows an expert 128 19.8 us, 208
+// 22.4; 128 rows 22.4 and 25.2; 160 rows 30.0 and 26.1; 256 rows 36.4 and 39.0; 400 rows 60.3 and 48.5.
 template <int MODE>
 cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
 {
