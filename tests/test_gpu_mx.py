@@ -183,6 +183,8 @@ MM = [
     # experts with many rows (pairs of CTAs), each pitch of the scale rows, one and many K tiles
     ([208], 256, 128), ([209, 300], 136, 768), ([416, 0, 1, 1000], 640, 512), ([150] * 7, 128, 2048),
     ([257, 129], 2056, 896), ([2000], 384, 256),
+    # more than 32 tiles for each pair of CTAs, and more than 64
+    ([3, 0, 20] * 100, 4096, 128), ([1] * 320, 4104, 256),
 ]
 
 
@@ -344,6 +346,7 @@ FFN = [
     (1, 1, 1, 128, 128), (1, 8, 2, 256, 384), (3, 128, 8, 256, 128), (16, 8, 2, 256, 512),
     (17, 4, 3, 384, 640), (40, 1024, 16, 128, 128), (64, 32, 8, 896, 256), (100, 8, 2, 384, 640),
     (257, 2, 1, 256, 128), (600, 4, 2, 256, 256), (1100, 16, 4, 256, 256), (8, 128, 8, 2048, 768),
+    (400, 300, 3, 128, 2048),  # more than 64 tiles of w13 for each pair of CTAs
 ]
 
 
