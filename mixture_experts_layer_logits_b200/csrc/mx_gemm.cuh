@@ -283,8 +283,10 @@ __device__ __forceinline__ bool tile_row_is_up(int r) { return r / 32 % 2; }
 // L1 line lookup and a 32-byte sector each time (as cp.async copies that was 0.58 of the 2.53 ms
 // of the FFN at T = 8192), so a row is read a group of 8 K tiles at a time (32 bytes; in 16-byte loads
 // where the row pitch allows it) into registers, one group ahead, and stored 4 bytes a stage.
-// The rows are split over four warps: a stage costs a warp some 200 cycles whatever it stores
-// (the fence towards tcgen05.cp's proxy, the arrival), which must stay under its 410.
+// The rows are split over four warps: a stage costs a warp some 200 cycles whatever it stores (the
+// wait, the fence towards tcgen05.cp's proxy, the arrival), and the fence waits for the loads ahead
+// too, 440 cycles a stage in all at T = 8192 (where a K tile takes 540 to 580).  Loads later in the
+// group cost 10%, several stages under one fence 4% (T = 64, E = 256).
 //   units       unit0, unit0 + stride, ... below `units`, each of num_kt K tiles
 //   kRows       rows of this thread; put[i]: where row i's bytes go within a stage's scales,
 //               or -1
