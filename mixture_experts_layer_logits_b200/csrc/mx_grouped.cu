@@ -145,6 +145,13 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity)
     return ok != 0;
 }
 
+// Arrives on the barrier once every cp.async this thread issued so far has landed: one of the
+// arrivals that the barrier counts.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
 // 16 TMEM lanes x 8 columns: lane i gets columns 2 (i % 4) and the next of TMEM lanes i / 4
 // (r[0], r[1]) and i / 4 + 8 (r[2], r[3]).
 __device__ __forceinline__ void tmem_ld_16x256(uint32_t taddr, uint32_t* r)
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // relayed one for its gathered rows
             mbar_init(&aux->full[s], 1 + 2 * kScaleWarps + (MODE == 0 ? 1 : 0));
             mbar_init(&aux->empty[s], 1);
-            mbar_init(&aux->gathered[s], kGatherWarps);
+            mbar_init(&aux->gathered[s], 32 * kGatherWarps);
         }
         for (int b = 0; b < kNBuf; ++b) {
             mbar_init(&aux->tfull[b], 1);
@@ -522,9 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (src[i])
                         cp_async_16_hint(sb + j * 128 + (((c & 7) ^ (j & 7)) << 4), src[i] + kt * kBK, pol);
                 }
-                cp_async_mbar_arrive(&aux->gathered[stage]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&aux->gathered[stage]);
+                cp_async_arrive(&aux->gathered[stage]);
             }
         }
         cp_async_commit();
