@@ -546,6 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0) arrive_leader(&aux->tempty[b]);
         };
         int lu = 0;
+        bool stopped = false;
         for (int u = unit0; u < units; u += stride, ++lu) {
             const Unit t = list.next();
             const int b = lu % kNBuf;
@@ -565,7 +566,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool got = mbar_wait(&aux->tfull[b], (uint32_t)((lu / kNBuf) & 1), abort_flag);
             if (!got) flag_error();
             // same in all 4 warps; also: the group is done with the unit before's staging
-            if (named_bar_or(1 + grp, 128, !got || *abort_flag)) break;
+            stopped = named_bar_or(1 + grp, 128, !got || *abort_flag);
+            if (stopped) break;
             __syncwarp();
             tc_fence_after();
             const uint32_t acc = tmem_base + ((uint32_t)(lq * 32) << 16) + (uint32_t)(b * NT);
@@ -687,11 +689,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();  // the buffers are free again
             }
         }
+        if (warp == kEpiWarp0) {
+            // CTA 0 commits to both CTAs, and nothing else waits for the last arrivals in CTA 1, nor
+            // for the ring's last ones in either: they must be in before the shared memory goes to
+            // another CTA.  A lane for each stage's last fill and one for the last commit of all.
+            // (After an abort the number of fills is not known; the last commit comes all the same,
+            // at most one bounded wait after this CTA's own.)
+            volatile int never = 0;
+            const int fills = lu * num_kt;
+            bool in = true;
+            if (lane < kStages && !stopped && fills > lane)
+                in = mbar_wait(&aux->empty[lane], (uint32_t)(((fills - lane - 1) / kStages) & 1), &never);
+            if (lane == kStages) in = mbar_wait(&aux->drain, 0, &never, 3000000000ull);
+            if (!in) flag_error();
+            __syncwarp();
+        }
     }
 
+    // Neither CTA leaves before the other's threads have made their last arrival in it; tensor-core
+    // arrivals are no thread's, and were waited for above.
     tc_fence_before();
     cluster_arrive();
-    cluster_wait();  // neither CTA leaves while the other may arrive on its barriers
+    cluster_wait();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
