@@ -295,6 +295,8 @@ __device__ __forceinline__ bool tile_row_is_up(int r) { return r / 32 % 2; }
 //   wait(q)     waits until ring fill q may be written (false: give up)
 //   stage(q)    shared memory of that fill's scales
 //   arrive(q)   called by every lane after its warp's stores are fenced
+// The launch before, which may still run when this one begins, may have written the scales (act's, or
+// those of a quantised matrix), so the loads are coherent ones; they follow the wait for that launch.
 constexpr int kScaleWarps = 4;
 template <int kRows, typename Fetch, typename Sources, typename Wait, typename Stage, typename Arrive>
 __device__ __forceinline__ void run_scales(int unit0, int stride, int units, int num_kt, int row_bytes,
@@ -314,20 +316,20 @@ __device__ __forceinline__ void run_scales(int unit0, int stride, int units, int
 #pragma unroll
                 for (int j = 0; j < 8; j += 4)
                     if (kt + j < num_kt) {
-                        const uint4 v = __ldg(reinterpret_cast<const uint4*>(s + 4 * j));
+                        const uint4 v = __ldca(reinterpret_cast<const uint4*>(s + 4 * j));
                         next[i][j] = v.x, next[i][j + 1] = v.y, next[i][j + 2] = v.z, next[i][j + 3] = v.w;
                     }
             } else if (align == 8) {
 #pragma unroll
                 for (int j = 0; j < 8; j += 2)
                     if (kt + j < num_kt) {
-                        const uint2 v = __ldg(reinterpret_cast<const uint2*>(s + 4 * j));
+                        const uint2 v = __ldca(reinterpret_cast<const uint2*>(s + 4 * j));
                         next[i][j] = v.x, next[i][j + 1] = v.y;
                     }
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    if (kt + j < num_kt) next[i][j] = __ldg(reinterpret_cast<const uint32_t*>(s + 4 * j));
+                    if (kt + j < num_kt) next[i][j] = __ldca(reinterpret_cast<const uint32_t*>(s + 4 * j));
             }
         }
     };
