@@ -49,6 +49,9 @@
  *   - The workspace is device memory of at least moe_workspace_size(shape) bytes,
  *     256-byte aligned, owned by the caller; calls that share one workspace must
  *     be ordered on one stream.  Its contents need no initialisation.
+ *   - Calls can be captured into a CUDA graph and replayed, also on new contents of
+ *     the same buffers (moe_device_status and the self-test excepted).  A captured call that
+ *     synchronises CTAs through its workspace clears those words by a memset node of its own.
  */
 #ifndef MOE_B200_H
 #define MOE_B200_H

@@ -52,10 +52,10 @@ struct Tile {
 };
 
 // The grid barrier of the multi-CTA permutation (32 bytes of device memory;
-// needs no initialisation).  CTA 0 of a call zeroes `count`, then publishes the
-// call's generation in `gen` (release); every CTA waits for that before its
-// first arrival.  A CTA that gives up on a wait stores the call's generation in
-// `abort`, so the others stop too.
+// needs no initialisation, but clear_generations in captured calls).  CTA 0 of
+// a call zeroes `count`, then publishes the call's generation in `gen` (release);
+// every CTA waits for that before its first arrival.  A CTA that gives up on a
+// wait stores the call's generation in `abort`, so the others stop too.
 struct GridBar {
     uint32_t count;
     uint32_t pad;
@@ -80,8 +80,14 @@ struct PermuteAux {
 // A value unique to each call that synchronises CTAs through workspace words
 // (the one-launch FFN, the multi-CTA permutation): a per-process random start
 // plus a counter, so that neither an earlier call's value nor stale workspace
-// bytes match it.
+// bytes match it (replays of a captured call: clear_generations).
 unsigned long long next_generation();
+
+// Clears the words that hold generations before the launch that uses them, if `st`
+// is being captured.  A graph repeats its calls' generations at each replay, and a
+// replay must not take the one before for its own: its CTAs would pass barriers
+// with the old counts and read what was published for the old inputs.
+cudaError_t clear_generations(void* words, size_t bytes, cudaStream_t st);
 
 // Streaming multiprocessors of the current device (cached per device).
 int device_sms();

@@ -178,6 +178,16 @@ unsigned long long next_generation()
     return counter.fetch_add(0x9E3779B97F4A7C15ull) + 0x9E3779B97F4A7C15ull;
 }
 
+cudaError_t clear_generations(void* words, size_t bytes, cudaStream_t st)
+{
+    cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(st, &status) != cudaSuccess) {
+        (void)cudaGetLastError();  // the launch that follows meets and reports it
+        return cudaSuccess;
+    }
+    return status == cudaStreamCaptureStatusActive ? cudaMemsetAsync(words, 0, bytes, st) : cudaSuccess;
+}
+
 namespace {
 
 PermuteAux make_aux(void* ws, const Layout& L, const moe_shape_t& s)
@@ -207,8 +217,8 @@ moe_status_t run_permute(const float* logits, int32_t* ids, float* weights, cons
         e = launch_small_route_permute(logits, s.T, s.E, s.top_k, ids, weights, offsets, rows, aux,
                                        st);
     } else {
-        e = cudaSuccess;
-        if (logits) e = launch_route(logits, s.T, s.E, s.top_k, ids, weights, st);
+        e = clear_generations(aux.bar, sizeof(GridBar), st);
+        if (e == cudaSuccess && logits) e = launch_route(logits, s.T, s.E, s.top_k, ids, weights, st);
         if (e == cudaSuccess) e = launch_large_permute(ids, s.T, s.E, s.top_k, offsets, rows, aux, st);
     }
     return cuda_status(e);
@@ -441,6 +451,8 @@ static moe_status_t forward_impl(const moe_bf16_t* x, const float* logits, const
         b.err = at<int32_t>(ws, L.err);
         FfnPlan plan = L.plan;
         plan.grid = device_sms();
+        if (r == MOE_OK)  // `ready`, and behind it the tokens' maxima with their generations
+            r = cuda_status(clear_generations(b.ready, L.xmax + (size_t)s.T * 16 - L.ready, st));
         if (r == MOE_OK)
             r = cuda_status(launch_fused_ffn(b, s.T, s.E, s.top_k, s.H, s.I, plan, st));
         for (int i = 2; i <= 4 && r == MOE_OK; ++i) r = mark(i);
@@ -646,12 +658,7 @@ moe_status_t moe_forward_mx4(const uint8_t* x, const uint8_t* x_scale, const flo
     int32_t* offs = expert_offsets ? expert_offsets : at<int32_t>(ws, L.route.offsets);
     int32_t* rows = permuted_rows ? permuted_rows : at<int32_t>(ws, L.route.rows);
     void* y = at<void>(ws, L.y);
-    moe_status_t r = MOE_OK;
-    // The multi-CTA permutation tells its calls apart by a generation that a captured graph
-    // repeats; cleared, a replay cannot take the one before for its own.
-    if (s.T * (long long)s.top_k > kSmallRows)
-        r = cuda_status(cudaMemsetAsync(at<void>(ws, L.route.bar), 0, sizeof(GridBar), st));
-    if (r == MOE_OK) r = run_permute(logits, ids, wts, s, offs, rows, ws, L.route, st);
+    moe_status_t r = run_permute(logits, ids, wts, s, offs, rows, ws, L.route, st);
     if (r == MOE_OK)
         r = run_ffn_mx4(x, x_scale, w13, w13_scale, w2, w2_scale, offs, rows, s, y, ws, L, st);
     if (r == MOE_OK) r = cuda_status(launch_combine(y, wts, s.T, s.top_k, s.H, out, st));

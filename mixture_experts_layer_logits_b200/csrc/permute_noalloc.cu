@@ -92,6 +92,8 @@ extern "C" moe_status_t moe_permute_noalloc(const int32_t* topk_ids, moe_shape_t
             e = launch_small_route_permute(nullptr, s.T, s.E, s.top_k, ids, nullptr,
                                            expert_offsets, permuted_rows, aux, st);
         else
+            e = clear_generations(aux.bar, sizeof(GridBar), st);
+        if (e == cudaSuccess && R > kSmallRows)
             e = launch_large_permute(ids, s.T, s.E, s.top_k, expert_offsets, permuted_rows, aux,
                                      st);
     }

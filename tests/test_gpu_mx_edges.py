@@ -1,5 +1,6 @@
 """The microscaled operators at the edges of what they accept: launches that follow each other at once,
 values at the ends of the range, captured calls (64-bit forms and bounds of mx_ref.py)."""
+import ctypes
 import os
 import sys
 
@@ -7,6 +8,7 @@ import pytest
 import torch
 
 import mixture_experts_layer_logits_b200 as moe
+from mixture_experts_layer_logits_b200 import workloads as wl
 
 sys.path.insert(0, os.path.dirname(os.path.abspath(__file__)))
 import mx_ref as ref
@@ -73,3 +75,107 @@ def test_launches_that_follow_each_other_at_once():
     for _, ws, y, first in calls:
         assert moe.moe_device_status(ws) == moe.MOE_OK
         assert torch.equal(y, first)
+
+
+# ------------------------------------------------------------------ captured calls on new inputs
+
+
+def replayed(call, refill, rounds=4):
+    """Captures call() and replays it on new contents of its inputs, twice in a row each time; yields its outputs
+    beside those of an uncaptured call."""
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call()
+    for i in range(rounds):
+        refill(i)
+        graph.replay()
+        graph.replay()
+        yield [t.clone() for t in outs], call()
+
+
+def distinct_ids(T, E, k, seed):
+    return torch.topk(randn(T, E, g=gen(seed)), k, dim=1).indices.to(I32)
+
+
+def sorted_by_expert(ids, E):
+    flat = ids.flatten().long()
+    counts = torch.bincount(flat, minlength=E)
+    return offsets_of(counts.tolist()), torch.argsort(flat, stable=True).to(I32)
+
+
+@pytest.mark.parametrize("T,E,k", [(60, 64, 8), (700, 64, 8), (9000, 300, 4)])
+@pytest.mark.parametrize("noalloc", [False, True])
+def test_captured_permutation_on_new_ids(T, E, k, noalloc):
+    ids = distinct_ids(T, E, k, 1)
+    ws = moe.workspace(T, E, k)
+
+    def call():
+        if not noalloc:
+            return moe.moe_permute(ids, E, ws=ws)
+        off = torch.empty(E + 1, dtype=I32, device="cuda")
+        rows = torch.empty(T * k, dtype=I32, device="cuda")
+        lib = moe.load_library()
+        lib.moe_permute_noalloc.argtypes = [ctypes.c_void_p, moe.Shape] + [ctypes.c_void_p] * 3
+        assert lib.moe_permute_noalloc(ids.data_ptr(), moe.Shape(T, E, k, 0, 0), off.data_ptr(), rows.data_ptr(),
+                                       torch.cuda.current_stream().cuda_stream) == moe.MOE_OK
+        return off, rows
+
+    # skewed and even in turn, so that counts of the replay before would be far off
+    def refill(i):
+        ids.copy_(distinct_ids(T, E, k, 10 + i) if i % 2 else torch.arange(k, dtype=I32, device="cuda").expand(T, k))
+
+    for got, again in replayed(call, refill):
+        for a, b, want in zip(got, again, sorted_by_expert(ids, E)):
+            assert torch.equal(a, want) and torch.equal(b, want)
+    assert moe.moe_device_status(ws) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("kind,T", [("bf16", 8), ("bf16", 64), ("bf16", 700), ("w8", 1), ("w8", 8), ("w8", 64),
+                                    ("mx4", 8), ("mx4", 700), ("steps", 700)])
+def test_captured_layer_on_new_inputs(kind, T):
+    """Inputs whose size changes by powers of two from replay to replay, so that a row scaled by what the
+    replay before had published would be far off or saturate."""
+    E, k, H, I = 16, 8, 256, 256
+    w = wl.custom("cap", T, E, k, H, I)
+    w13, w2 = wl.make_weights(w, seed=3, device="cuda")
+    x, logits = randn(T, H, g=gen(4)).to(BF16), randn(T, E, g=gen(5))
+    ws = moe.workspace(T, E, k, H, I)
+    if kind == "w8":
+        g = gen(6)
+        c13 = torch.randint(0, 120, tuple(w13.shape), generator=g, device="cuda", dtype=U8)
+        c2 = torch.randint(0, 120, tuple(w2.shape), generator=g, device="cuda", dtype=U8)
+        s13 = torch.rand(E, 2 * I, generator=g, device="cuda") * 2.0 ** -12
+        s2 = torch.rand(E, H, generator=g, device="cuda") * 2.0 ** -12
+    if kind in ("mx4", "steps"):
+        experts = (*moe.moe_quantize_mx(w13), *moe.moe_quantize_mx(w2))
+        ws = moe.workspace_mx4(T, E, k, H, I)
+
+    def call():
+        if kind == "bf16":
+            return [moe.moe_forward(x, logits, w13, w2, k, ws=ws)]
+        if kind == "w8":
+            return [moe.moe_forward_w8(x, logits, c13, s13, c2, s2, k, ws=ws)]
+        q, s = moe.moe_quantize_mx(x, "e4m3")
+        if kind == "mx4":
+            return [moe.moe_forward_mx4(q, s, logits, *experts, k, ws=ws)]
+        ids, p = moe.moe_route(logits, k)
+        off, rows = moe.moe_permute(ids, E)
+        y = moe.moe_grouped_ffn_mx4(q, s, *experts, off, rows, k, ws=ws)
+        return [moe.moe_combine(y, p), off, rows]
+
+    def refill(i):
+        x.copy_(randn(T, H, g=gen(20 + i)) * 2.0 ** (6 * (i % 2) - 3))
+        logits.copy_(randn(T, E, g=gen(40 + i)) * (1 + 9 * (i % 2)))
+
+    last = None
+    for got, again in replayed(call, refill):
+        for a, b in zip(got, again):
+            assert torch.equal(a, b)
+        assert moe.moe_device_status(ws) == moe.MOE_OK
+        assert last is None or not torch.equal(got[0], last)
+        last = got[0]
