@@ -254,6 +254,7 @@ moe_status_t moe_quantize_mx(const void* src, int src_type, int64_t rows, int64_
  * H columns, in fp32 -> sum = h, out = bf16(n), codes / scales = n in MX E4M3
  * blocks (quantised from the fp32 n, not from out).  x, residual, sum and out bf16
  * [T, H], weight bf16 [H].  Without a residual (NULL, then sum is NULL too) h = x.
+ * Finite rows of any size are normed, those whose squares fp32 cannot hold too.
  * out may be NULL, or codes and scales may (both), not all three.  sum may be the
  * residual's own buffer; nothing else may alias.
  *   T < 1, H < 32, H > 65536 or H not a multiple of 32 -> MOE_ERR_UNSUPPORTED_SHAPE

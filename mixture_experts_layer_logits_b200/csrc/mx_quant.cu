@@ -79,12 +79,29 @@ __global__ void __launch_bounds__(256)
 
 // ------------------------------------------------------------------ norm
 
+// The sum of v over the CTA, in every thread.  `part`: 32 floats of shared memory.
+__device__ __forceinline__ float block_sum(float v, float* part)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // One row per CTA.  h = x + residual rounded to bf16 (that is what the next layer
 // reads, so the norm is the norm of the stored sum), r = 1 / sqrt(mean(h^2) + eps),
 // n = (h * weight) * r: the product of two bf16 values is exact in fp32, so n carries
-// the rounding of r and of one product.  Sums are fp32.
-template <int C>
-__global__ void __launch_bounds__(1024)
+// the rounding of r and of one product.  Sums are fp32.  h first takes the power of two that
+// brings the root mean square to 2^-14 .. 2^-13, and r the opposite one: h * weight is then out of
+// fp32's range only where n is, or is below bf16's.
+// kThreads, kMin: the most threads of a CTA, and CTAs an SM has to hold (2048 x 8192, C = 4: registers for
+// five CTAs of 256 threads 18.6 us, for six 17.1).
+template <int C, int kThreads, int kMin>
+__global__ void __launch_bounds__(kThreads, kMin)
     rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int chunks, float inv_h, float eps,
                    uint4* sum, uint4* __restrict__ out, uint8_t* __restrict__ codes,
                    uint8_t* __restrict__ scales)
@@ -95,9 +112,9 @@ __global__ void __launch_bounds__(1024)
     const size_t base = (size_t)blockIdx.x * chunks;
     uint4 h[C];
     float ss = 0.f;
-    // Chunks whose loads are in flight together (8192 x 4096 with residual: one by one 51.1 us, two at
-    // a time 46.6; 64 x 65536 14.1 and 12.5).  At C = 8 the registers hold no more.
-    constexpr int kBatch = C < 2 ? C : 2;
+    // Chunks whose loads are in flight together (8192 x 4096 with residual: one by one 51.1 us, two
+    // 46.6; 2048 x 8192: two 17.7, four 17.1).  At C = 8 the registers hold no more than two.
+    constexpr int kBatch = C < 8 ? C : 2;
 #pragma unroll
     for (int i0 = 0; i0 < C; i0 += kBatch) {
         uint4 add[kBatch];
@@ -105,8 +122,8 @@ __global__ void __launch_bounds__(1024)
         for (int i = 0; i < kBatch; ++i) {
             const int c = threadIdx.x + (i0 + i) * blockDim.x;
             if (c >= chunks) continue;
-            h[i0 + i] = __ldca(x + base + c);
-            if (residual) add[i] = __ldca(residual + base + c);
+            h[i0 + i] = __ldcs(x + base + c);
+            if (residual) add[i] = __ldcs(residual + base + c);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -127,14 +144,27 @@ __global__ void __launch_bounds__(1024)
             for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
         }
     }
+    float m = fmaf(block_sum(ss, part), inv_h, eps), scale = 1.0f;
+    if (!(m >= 0x1p-100f && m < INFINITY)) {  // the same in every thread
+        // Squares left the range of fp32, or they and eps lie so low that what underflowed would
+        // count: once more for the row times a power of two (a NaN or an infinity stays one).
+        scale = m < 1.0f ? 0x1p80f : 0x1p-80f;
+        ss = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = ss;
-    __syncthreads();
-    ss = (threadIdx.x & 31) < (blockDim.x >> 5) ? part[threadIdx.x & 31] : 0.f;
+        for (int i = 0; i < C; ++i) {
+            if (threadIdx.x + i * blockDim.x >= chunks) continue;
+            float v[8];
+            unpack_bf16x8(h[i], v);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = 1.0f / sqrtf(fmaf(ss, inv_h, eps));
+            for (int j = 0; j < 8; ++j) ss = fmaf(v[j] * scale, v[j] * scale, ss);
+        }
+        __syncthreads();  // `part` has been read
+        m = fmaf(block_sum(ss, part), inv_h, eps * scale * scale);
+    }
+    // m = f 4^k with f in [1/4, 1).  The 2^-13 keeps `down` in range for a row of one element 2^-133.
+    const int k = ((int)(__float_as_uint(m) >> 23 & 255) - 127 + 2) >> 1;
+    const float down = scale * __uint_as_float((uint32_t)(127 - 13 - k) << 23);
+    const float r = 1.0f / sqrtf(m) * __uint_as_float((uint32_t)(127 + 13 + k) << 23);
 #pragma unroll
     for (int i = 0; i < C; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
@@ -145,7 +175,7 @@ __global__ void __launch_bounds__(1024)
             unpack_bf16x8(h[i], v);
             unpack_bf16x8(__ldca(weight + c), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = (v[j] * w[j]) * r;
+            for (int j = 0; j < 8; ++j) v[j] = (v[j] * down * w[j]) * r;
             if (out) out[base + c] = pack_bf16x8(v);
         }
         if (codes) {
@@ -159,10 +189,10 @@ __global__ void __launch_bounds__(1024)
     }
 }
 
-template <int C>
+template <int C, int kThreads, int kMin>
 cudaError_t launch_norm(const NormArgs& a, int threads, cudaStream_t st)
 {
-    return launch_pdl(rmsnorm_kernel<C>, dim3(a.T), dim3(threads), 0, st,
+    return launch_pdl(rmsnorm_kernel<C, kThreads, kMin>, dim3(a.T), dim3(threads), 0, st,
                       static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.residual),
                       static_cast<const uint4*>(a.weight), a.H / 8, 1.0f / (float)a.H, a.eps,
                       static_cast<uint4*>(a.sum), static_cast<uint4*>(a.out), a.codes, a.scales);
@@ -182,10 +212,10 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st)
     const int c = (chunks + most - 1) / most;
     const int cc = c <= 1 ? 1 : c <= 2 ? 2 : c <= 4 ? 4 : 8;
     const int threads = ((chunks + cc - 1) / cc + 31) & ~31;
-    if (cc == 1) return launch_norm<1>(a, threads, st);
-    if (cc == 2) return launch_norm<2>(a, threads, st);
-    if (cc == 4) return launch_norm<4>(a, threads, st);
-    return launch_norm<8>(a, threads > 1024 ? 1024 : threads, st);
+    if (cc == 1) return launch_norm<1, 1024, 2>(a, threads, st);
+    if (cc == 2) return launch_norm<2, 1024, 2>(a, threads, st);
+    if (cc == 4) return most == 256 ? launch_norm<4, 256, 6>(a, threads, st) : launch_norm<4, 1024, 1>(a, threads, st);
+    return launch_norm<8, 1024, 1>(a, threads > 1024 ? 1024 : threads, st);
 }
 
 template <bool E2M1, typename Src, int U>

@@ -77,6 +77,80 @@ def test_launches_that_follow_each_other_at_once():
         assert torch.equal(y, first)
 
 
+# ------------------------------------------------------------------ norm: the whole range of bf16
+
+
+def check_norm(x, w, eps, residual=None):
+    h, out, codes, scales = moe.moe_add_rmsnorm(x, w, eps, residual=residual, quantize=True)
+    want_h, n, err = ref.rmsnorm(x, residual, w, eps)
+    if residual is not None:
+        assert torch.equal(h, want_h)
+    # Below its normal numbers fp32 rounds by up to 2^-150: h brought to a root mean square of 2^-13
+    # (an error that the weight and then r <= 2^14 multiply), its product with the weight (r), and n itself:
+    # 2^-136 (|w| + 1) + 2^-150.  bf16 rounds by up to 2^-134 there.
+    err = err + 2.0 ** -135 * (1 + w.to(ref.F64).abs())
+    ref.assert_within(out, n, err + ref.BF16_HALF_STEP * (n.abs() + err) + 2.0 ** -134, "out")
+    ref.assert_within(ref.decode(codes, scales, "e4m3"), ref.mx(n), ref.mx_shift(n, err), "codes")
+    return out
+
+
+@pytest.mark.parametrize("H", [32, 256, 4128, 65536])
+@pytest.mark.parametrize("eps", [1e-6, 0.0, 1e-38])
+def test_norm_of_rows_of_any_size(H, eps):
+    """Rows scaled by 2^-120 .. 2^124, on both sides of where a sum of H squares overflows (2^64 / sqrt(H)) and
+    underflows fp32."""
+    e = torch.tensor([-120, -100, -80, -76, -66, -62, -50, -45, -20, 0, 40, 52, 55, 56, 57, 59, 60, 61, 63, 64, 65,
+                      80, 100, 120, 124], device="cuda")
+    x = randn(len(e), H, g=gen(70)).clamp(-4, 4).to(BF16)
+    x = torch.ldexp(x.to(ref.F64), e[:, None]).to(BF16)
+    w = (1 + 0.3 * randn(H, g=gen(71))).to(BF16)
+    check_norm(x, w, eps)
+
+
+@pytest.mark.parametrize("H", [32, 4128])
+def test_norm_without_eps_does_not_depend_on_a_power_of_two(H):
+    """One row times 2^-100 .. 2^120: every step scales exactly, so the norms are the same bits."""
+    e = torch.arange(-100, 121, device="cuda")
+    row = randn(1, H, g=gen(75)).clamp(-4, 4).to(BF16)
+    x = torch.ldexp(row.to(ref.F64).expand(len(e), H), e[:, None]).to(BF16)
+    w = (1 + 0.3 * randn(H, g=gen(76))).to(BF16)
+    out = check_norm(x, w, 0.0)
+    assert torch.equal(out, out[100:101].expand_as(out))
+
+
+@pytest.mark.parametrize("T", [1, 5, 1100])
+def test_norm_of_few_huge_or_tiny_elements(T):
+    """One element that decides the row, beside ordinary ones, with the largest and smallest of bf16."""
+    H = 4128
+    top = torch.finfo(BF16).max
+    for value in (top, -top, 2.0 ** 66, 2.0 ** 57):
+        x = randn(T, H, g=gen(72)).to(BF16)
+        x[T // 2, 77] = value
+        check_norm(x, torch.ones(H, dtype=BF16, device="cuda"), 1e-6)
+    x = torch.zeros(T, H, dtype=BF16, device="cuda")
+    x[:, 5] = 2.0 ** -133
+    check_norm(x, torch.ones(H, dtype=BF16, device="cuda"), 0.0)
+    x[:] = top
+    check_norm(x, torch.ones(H, dtype=BF16, device="cuda"), 1e-6, residual=torch.zeros_like(x))
+
+
+@pytest.mark.parametrize("size", [-50, -10, 0, 40, 70, 110])
+def test_norm_with_weights_of_any_size(size):
+    """The product of a row and its weights may pass fp32's range where the norm does not."""
+    H = 512
+    x = torch.ldexp(randn(3, H, g=gen(73)).to(BF16), torch.tensor(size, device="cuda"))
+    we = torch.tensor([-120, -90, -60, 0, 60, 90, 110, 124], device="cuda").repeat_interleave(64)
+    w = torch.ldexp(1 + 0.3 * randn(H, g=gen(74)).clamp(-2, 2), we).to(BF16)
+    check_norm(x, w, 1e-30)
+
+
+def test_norm_of_zero_rows_without_eps_is_nan():
+    x = torch.zeros(2, 64, dtype=BF16, device="cuda")
+    x[1] = 1
+    _, out, _, scales = moe.moe_add_rmsnorm(x, x[1].clone(), 0.0, quantize=True)
+    assert bool(torch.isnan(out[0]).all()) and bool((scales[0] == 255).all()) and bool((out[1] == 1).all())
+
+
 # ------------------------------------------------------------------ captured calls on new inputs
 
 
