@@ -172,14 +172,19 @@ __device__ __forceinline__ void store_matrix_x4_trans(uint32_t addr, uint32_t a,
                  : "memory");
 }
 
-// silu(g) u = g u / (1 + 2^(-g log2 e)).  Exponential and reciprocal are one instruction each, a few
-// ulp of fp32, far inside the rounding to E4M3; where the power overflows the reciprocal is 0.
+// silu(g) u = g u / (1 + 2^(-g log2 e)), exponential and reciprocal one instruction each.  The
+// rounding of the exponent makes the power off by up to |g| units of 2^-24, and instructions and
+// products add a few of 2^-23: far inside the rounding to E4M3.  From g = -64 down 1 / (1 + e^-g) is
+// e^g to fp32's precision and is taken as the square of 2^(g log2 e / 2), one factor of it with u.
+// The reciprocal would be subnormal from g = -87.3 on, hence zero; this holds to g = -174,
+// where e^g = 2^-251.  It costs the prompt's FFN 0.3% (T = 8192: 1311 and 1316 us).
 __device__ __forceinline__ float swiglu(float g, float u)
 {
+    const bool far = !(g > -64.0f);
     float p, r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * -1.44269504f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(g * (far ? 0.72134752f : -1.44269504f)));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + p));
-    return g * r * u;
+    return g * (far ? p : r) * (far ? p * u : u);
 }
 
 // The largest magnitude of four, NaN if one of them is.

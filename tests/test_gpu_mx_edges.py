@@ -151,6 +151,42 @@ def test_norm_of_zero_rows_without_eps_is_nan():
     assert bool(torch.isnan(out[0]).all()) and bool((scales[0] == 255).all()) and bool((out[1] == 1).all())
 
 
+# ------------------------------------------------------------------ SwiGLU far from zero
+
+
+def test_swiglu_of_large_negative_gates():
+    """Gates and ups that the products give exactly, 32 features of each, so that act's error is that of the
+    activation alone: down to where e^g = 2^-251, with ups that bring the product back."""
+    gates = [6.0, -0.25, -16.0, -48.0, -63.0, -64.0, -65.0, -80.0, -87.0, -87.5, -88.0, -90.0, -96.0, -104.0, -152.0,
+             -174.0]
+    ups = [1.5, -2.0 ** 30, 3 * 2.0 ** 60, 2.0 ** 100]
+    H, blocks = 256, [(g, u) for g in gates for u in ups]
+    I = 32 * len(blocks)
+    w13 = torch.zeros(1, 2 * I, H, dtype=ref.F64)
+    for b, (g, u) in enumerate(blocks):
+        rest, at = abs(g), 0
+        while rest:  # a power of two, or 1.5 of one, in a block of columns of its own
+            p = 2.0 ** (int(rest).bit_length() - 1 if rest >= 1 else -2)
+            p = 1.5 * p if 1.5 * p <= rest else p
+            w13[0, 32 * b:32 * b + 32, 32 * at] = p if g > 0 else -p
+            rest, at = rest - p, at + 1
+        w13[0, I + 32 * b:I + 32 * b + 32, 5] = u
+    w2 = torch.zeros(1, H, I, dtype=ref.F64)
+    w2[0, torch.arange(H), 8 * torch.arange(H)] = 1   # four features of each block
+    (q13, s13), (q2, s2) = ref.quantize(w13.cuda(), "e2m1"), ref.quantize(w2.cuda(), "e2m1")
+    assert torch.equal(ref.decode(q13, s13, "e2m1"), w13.cuda())
+    T = 3
+    x = torch.tensor([1.0, 0.5, 1.0], dtype=ref.F64, device="cuda")[:, None].expand(T, H)
+    qx, sx = ref.quantize(x, "e4m3")
+    off, rows = offsets_of([T]), torch.arange(T, dtype=I32, device="cuda")
+    y = moe.moe_grouped_ffn_mx4(qx, sx, q13, s13, q2, s2, off, rows, 1)
+    h = x @ w13.cuda()[0].T
+    act, err = ref.swiglu(h, torch.zeros_like(h))
+    err = err + 2.0 ** -149   # a product below fp32's normal numbers
+    want, tol = ref.grouped_mm(ref.mx(act), q2, s2, off, ref.mx_shift(act, err))
+    ref.assert_within(y, want, tol + 2.0 ** -134, "y")   # half a step of bf16 below its normal numbers
+
+
 # ------------------------------------------------------------------ captured calls on new inputs
 
 
