@@ -35,12 +35,12 @@
  *     dependent launch; set MOE_DISABLE_PDL=1 in the environment to turn it off.
  *   - All arguments are validated on the host before anything is launched; on an
  *     error no work is queued and no output is touched:
- *       NULL pointer                                      -> MOE_ERR_INVALID_ARG
+ *       NULL pointer, or a value that its call excludes    -> MOE_ERR_INVALID_ARG
  *       T < 1, E < 1 or E > 1024, k < 1 or k > min(E, 16) -> MOE_ERR_UNSUPPORTED_SHAPE
  *       (ffn/combine/forward) H or I < 128 or not a multiple of 128
  *                                                         -> MOE_ERR_UNSUPPORTED_SHAPE
  *       T*k > 2^30 or a size overflow                      -> MOE_ERR_UNSUPPORTED_SHAPE
- *       a base pointer not 16-byte aligned                 -> MOE_ERR_MISALIGNED
+ *       a base pointer not 16-byte aligned (E2M1 weights: 32) -> MOE_ERR_MISALIGNED
  *       ws_bytes < moe_workspace_size(shape)               -> MOE_ERR_WORKSPACE_TOO_SMALL
  *     A failed launch returns MOE_ERR_CUDA; moe_last_cuda_error() then gives the
  *     cudaError_t (per host thread).

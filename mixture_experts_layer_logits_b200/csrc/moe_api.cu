@@ -697,9 +697,9 @@ const char* moe_status_string(moe_status_t status)
 {
     switch (status) {
     case MOE_OK: return "ok";
-    case MOE_ERR_INVALID_ARG: return "invalid argument (null pointer)";
+    case MOE_ERR_INVALID_ARG: return "invalid argument (a null pointer, or a value outside its range)";
     case MOE_ERR_UNSUPPORTED_SHAPE: return "unsupported shape";
-    case MOE_ERR_MISALIGNED: return "pointer not 16-byte aligned";
+    case MOE_ERR_MISALIGNED: return "pointer not aligned (16 bytes; E2M1 weights 32)";
     case MOE_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case MOE_ERR_CUDA: return "CUDA error (see moe_last_cuda_error)";
     case MOE_ERR_DEVICE_TIMEOUT: return "a kernel gave up on a bounded wait";

@@ -23,3 +23,28 @@ def test_no_read_only_loads(path):
     text = code(path)
     assert "__ldg(" not in text and "ld.global.nc" not in text
     assert not re.search(r"const\s+\w+\s*\*\s*(const\s+)?__restrict__", text)
+
+
+@pytest.fixture(scope="module")
+def status_string():
+    import mixture_experts_layer_logits_b200 as moe
+    from mixture_experts_layer_logits_b200 import build
+
+    build.build()
+    return lambda status: moe.load_library().moe_status_string(status).decode()
+
+
+def test_the_alignment_error_names_both_rules(status_string):
+    """E2M1 weights that are 16-byte aligned only are refused with this status too."""
+    import mixture_experts_layer_logits_b200 as moe
+
+    text = status_string(moe.MOE_ERR_MISALIGNED)
+    assert "16" in text and "E2M1" in text and "32" in text
+    assert text in str(moe.MoeError(moe.MOE_ERR_MISALIGNED, "moe_grouped_mm_mx4"))
+
+
+def test_the_argument_error_is_not_only_of_null_pointers(status_string):
+    """A negative eps or an unknown format gets it as well."""
+    import mixture_experts_layer_logits_b200 as moe
+
+    assert "value" in status_string(moe.MOE_ERR_INVALID_ARG)
