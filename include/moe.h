@@ -268,6 +268,8 @@ moe_status_t moe_add_rmsnorm(const moe_bf16_t* x, const moe_bf16_t* residual,
  * <= r < expert_offsets[e + 1], summed in fp32 and rounded once to bf16.  a MX E4M3
  * [R, K], w MX E2M1 [E, N, K], expert_offsets int32 [E + 1], ascending from 0 to at
  * most R -> y bf16 [R, N]; rows from expert_offsets[E] on are left as they were.
+ * Sums past fp32's or bf16's range are infinite; where partial sums of both signs pass
+ * fp32's, the infinity may be of either sign.  Subnormal results are not flushed.
  *   R < 1, R > 2^30, E < 1, E > 1024, N < 8 or not a multiple of 8, K < 128 or not a
  *   multiple of 128, or a size overflow                 -> MOE_ERR_UNSUPPORTED_SHAPE
  *   w not 32-byte aligned (others: 16)                  -> MOE_ERR_MISALIGNED

@@ -2,6 +2,7 @@
 values at the ends of the range, captured calls (64-bit forms and bounds of mx_ref.py)."""
 import ctypes
 import os
+import subprocess
 import sys
 
 import pytest
@@ -149,6 +150,94 @@ def test_norm_of_zero_rows_without_eps_is_nan():
     x[1] = 1
     _, out, _, scales = moe.moe_add_rmsnorm(x, x[1].clone(), 0.0, quantize=True)
     assert bool(torch.isnan(out[0]).all()) and bool((scales[0] == 255).all()) and bool((out[1] == 1).all())
+
+
+# ------------------------------------------------------------------ products: the whole range of scales
+
+
+def draw_codes(R, N, K, seed):
+    g = gen(seed)
+    a = torch.randint(0, 0x7F, (R, K), generator=g, device="cuda", dtype=U8)   # not negative
+    w = torch.randint(0, 256, (1, N, K // 2), generator=g, device="cuda", dtype=U8)
+    return a, w
+
+
+def under_scales(a, w, sa, sw):
+    A = torch.full((a.shape[0], a.shape[1] // 32), sa, dtype=U8, device="cuda")
+    W = torch.full((1, w.shape[1], w.shape[2] // 16), sw, dtype=U8, device="cuda")
+    y = moe.moe_grouped_mm_mx4(a, A, w, W, offsets_of([a.shape[0]]))
+    want, tol = ref.grouped_mm(ref.decode(a, A, "e4m3"), w, W, offsets_of([a.shape[0]]))
+    return y, want, tol
+
+
+@pytest.mark.parametrize("R", [20, 300])
+@pytest.mark.parametrize("sa,sw", [(254, 254), (200, 240), (240, 140), (140, 240), (250, 127), (127, 250), (186, 186)])
+def test_products_past_the_largest_number_are_infinite(R, sa, sw):
+    """Rows of one sign, so that no partial sum is larger than the whole: past fp32's or bf16's range the
+    result is the infinity of its sign, and below it is the ordinary one."""
+    a, w = draw_codes(R, 136, 384, 80)
+    w &= 0x77
+    w[0, 1::2] |= 0x88                                   # odd features: all weights negative
+    y, want, tol = under_scales(a, w, sa, sw)
+    # bf16 rounds to infinity from 2^128 (1 - 2^-9) on; a sum that may lie on either side of that is not looked at
+    edge = 2.0 ** 128 * (1 - 2.0 ** -9)
+    over, under = want.abs() - tol >= edge, want.abs() + tol < edge
+    assert bool(over.any())
+    assert torch.equal(y[over].to(ref.F64), torch.sign(want[over]) * float("inf"))
+    ref.assert_within(y[under], want[under], tol[under], "y")
+
+
+@pytest.mark.parametrize("R", [20, 300])
+@pytest.mark.parametrize("sa,sw", [(1, 126), (100, 27), (60, 60), (0, 120), (120, 0), (40, 75), (10, 100), (40, 60),
+                                   (0, 0)])
+def test_products_below_the_smallest_normal_number(R, sa, sw):
+    """Weights and products of either sign under scales that bring the sums below bf16's and fp32's normal numbers.  There
+    each of K fp32 sums may round by 2^-149, and bf16 by half a step, 2^-134."""
+    K = 384
+    a, w = draw_codes(R, 136, K, 81)
+    y, want, tol = under_scales(a, w, sa, sw)
+    ref.assert_within(y, want, tol + K * 2.0 ** -149 + 2.0 ** -134, "y")
+
+
+# ------------------------------------------------------------------ the index checks of the debug build
+
+DEBUG_CHILD = """
+import sys, torch
+sys.path.insert(0, {root!r})
+import mixture_experts_layer_logits_b200 as moe
+from mixture_experts_layer_logits_b200 import workloads as wl
+assert moe.library_path == moe.debug_library_path
+T, E, k, H, I = {T}, 4, 2, 256, 256
+d = wl.make_inputs(wl.custom("dbg", T, E, k, H, I), seed=1, device="cuda")
+x, sx = moe.moe_quantize_mx(d["x"], "e4m3")
+experts = (*moe.moe_quantize_mx(d["w13"]), *moe.moe_quantize_mx(d["w2"]))
+off, rows = moe.moe_permute(moe.moe_route(d["logits"], k)[0], E)
+ws = moe.workspace_mx4(T, E, k, H, I)
+good = moe.moe_grouped_ffn_mx4(x, sx, *experts, off, rows, k, ws=ws)
+assert moe.moe_device_status(ws) == moe.MOE_OK
+at = {at} % rows.numel()
+lost = int(rows[at])
+rows[at] = {bad}
+y = torch.full_like(good, 7.0)
+moe.moe_grouped_ffn_mx4(x, sx, *experts, off, rows, k, ws=ws, y=y)
+assert moe.moe_device_status(ws) == moe.MOE_ERR_DEVICE_BOUNDS
+assert moe.moe_device_status(ws) == moe.MOE_OK
+# the bad position reads and writes row 0 instead; every other row is as it was, the lost one not written
+keep = torch.ones(T * k, dtype=torch.bool, device="cuda")
+keep[0] = keep[lost] = False
+assert torch.equal(y[keep], good[keep])
+assert lost == 0 or bool((y[lost] == 7.0).all())
+print("checked")
+"""
+
+
+@pytest.mark.parametrize("T,at,bad", [(1, 0, -1), (9, 1, 10 ** 9), (300, 1, -1), (300, -1, 600)])
+def test_debug_build_leaves_other_rows_alone(T, at, bad):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", DEBUG_CHILD.format(root=root, T=T, at=at, bad=bad)],
+                       env=dict(os.environ, MOE_LIBRARY="debug"), cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "checked" in r.stdout, r.stdout[-2000:] + r.stderr[-3000:]
 
 
 # ------------------------------------------------------------------ SwiGLU far from zero
