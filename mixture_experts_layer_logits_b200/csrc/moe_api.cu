@@ -251,11 +251,19 @@ moe_status_t run_ffn(const void* x, const void* w13, const void* w2, const int32
 // aligned tensors.
 bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
+// Rows of all experts' weights: TMA row coordinates, with room to round up to a pair's 256 features.
+constexpr long long kMaxMxRows = INT_MAX - 255;
+
+bool mx4_shape_ok(const moe_shape_t& s)
+{
+    return ffn_shape_ok(s) && (long long)s.E * s.H <= kMaxMxRows && (long long)s.E * 2 * s.I <= kMaxMxRows;
+}
+
 bool mm_shape_ok(const moe_mm_shape_t& s)
 {
     if (s.R < 1 || s.R > (1 << 30) || s.E < 1 || s.E > 1024) return false;
     if (s.N < 8 || s.N % 8 || s.K < 128 || s.K % 128) return false;
-    if ((long long)s.E * s.N > INT_MAX) return false;  // TMA row coordinates
+    if ((long long)s.E * s.N > kMaxMxRows) return false;
     return (long long)s.R * s.N <= (1LL << 40) && (long long)s.R * s.K <= (1LL << 40);
 }
 
@@ -612,7 +620,7 @@ moe_status_t moe_grouped_mm_mx4(const uint8_t* a, const uint8_t* a_scale, const 
 
 size_t moe_mx4_workspace_size(moe_shape_t s)
 {
-    return ffn_shape_ok(s) ? mx_layout_for(s).total : 0;
+    return mx4_shape_ok(s) ? mx_layout_for(s).total : 0;
 }
 
 moe_status_t moe_grouped_ffn_mx4(const uint8_t* x, const uint8_t* x_scale, const uint8_t* w13,
@@ -624,7 +632,7 @@ moe_status_t moe_grouped_ffn_mx4(const uint8_t* x, const uint8_t* x_scale, const
     if (!x || !x_scale || !w13 || !w13_scale || !w2 || !w2_scale || !expert_offsets ||
         !permuted_rows || !y || !ws)
         return MOE_ERR_INVALID_ARG;
-    if (!ffn_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!mx4_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x) || !aligned16(x_scale) || !aligned32(w13) || !aligned16(w13_scale) ||
         !aligned32(w2) || !aligned16(w2_scale) || !aligned16(expert_offsets) ||
         !aligned16(permuted_rows) || !aligned16(y) || !aligned16(ws))
@@ -644,7 +652,7 @@ moe_status_t moe_forward_mx4(const uint8_t* x, const uint8_t* x_scale, const flo
 {
     if (!x || !x_scale || !logits || !w13 || !w13_scale || !w2 || !w2_scale || !out || !ws)
         return MOE_ERR_INVALID_ARG;
-    if (!ffn_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!mx4_shape_ok(s)) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(x) || !aligned16(x_scale) || !aligned16(logits) || !aligned32(w13) ||
         !aligned16(w13_scale) || !aligned32(w2) || !aligned16(w2_scale) || !aligned16(out) ||
         !aligned16(ws) || !aligned16(topk_ids) || !aligned16(topk_weights) ||

@@ -25,6 +25,21 @@ def test_no_read_only_loads(path):
     assert not re.search(r"const\s+\w+\s*\*\s*(const\s+)?__restrict__", text)
 
 
+def test_feature_counts_that_cannot_be_rounded_up_are_refused():
+    """A pair of CTAs takes 256 features; a count within 255 of 2^31 would overflow when rounded up to that, and the
+    product would do nothing and report success."""
+    import mixture_experts_layer_logits_b200 as moe
+    from mixture_experts_layer_logits_b200 import build
+
+    build.build()
+    top = 2 ** 31 - 256
+    assert moe.moe_grouped_mm_workspace_size(1, 1, top, 128) > 0
+    assert moe.moe_grouped_mm_workspace_size(1, 1, 2 ** 31 - 8, 128) == 0
+    assert moe.moe_grouped_mm_workspace_size(1, 3, (2 ** 31 - 8) // 24 * 8, 128) == 0
+    assert moe.moe_mx4_workspace_size(1, 1, 1, top, 128) > 0
+    assert moe.moe_mx4_workspace_size(1, 1, 1, 2 ** 31 - 128, 128) == 0
+
+
 @pytest.fixture(scope="module")
 def status_string():
     import mixture_experts_layer_logits_b200 as moe
