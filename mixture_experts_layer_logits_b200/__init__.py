@@ -315,7 +315,9 @@ def moe_forward_fused(T: int, E: int, top_k: int, H: int, I: int) -> bool:
 # ------------------------------------------------------------------ microscaled operators
 #
 # These calls run on the current stream of their tensors' device, whichever device is
-# current, and check that all tensors are on that one.
+# current, and check that all tensors are on that one.  The word that moe_device_status reads lies
+# in the workspace: a program that wants to know of a bounded wait that ran out passes `ws`
+# (without one the call allocates its own and drops it).
 
 _MX_FORMATS = {"e2m1": 0, "e4m3": 1}
 _MX_SOURCES = {torch.bfloat16: 0, torch.float32: 1}
@@ -348,16 +350,23 @@ def _out_like(t, name, like, dtype):
     return t
 
 
+# The current device and a device's current stream without torch's wrappers around them, or the
+# public forms where a build of torch has no such entry.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, where, device, *args):
     """fn(*args, current stream of `device`) with that device current."""
     if device.type != "cuda":
         raise ValueError(f"{where}: expected CUDA tensors, got {device}")
     index = device.index
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _current_device():
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, _raw_stream(index))
     if status != MOE_OK:
         raise MoeError(status, where)
 

@@ -2,6 +2,8 @@
 import glob
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 
@@ -63,3 +65,23 @@ def test_the_argument_error_is_not_only_of_null_pointers(status_string):
     import mixture_experts_layer_logits_b200 as moe
 
     assert "value" in status_string(moe.MOE_ERR_INVALID_ARG)
+
+
+PUBLIC_ONLY = """
+import sys, torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+torch.cuda.current_device = lambda: 0
+torch.cuda.current_stream = lambda index: type("S", (), {"cuda_stream": 1234 + index})
+import mixture_experts_layer_logits_b200 as moe
+seen = []
+moe._call(lambda *a: seen.append(a) or moe.MOE_OK, "f", torch.device("cuda", 0), 7)
+assert seen == [(7, 1234)], seen
+print("called")
+"""
+
+
+def test_calls_without_torchs_private_entries():
+    r = subprocess.run([sys.executable, "-c", PUBLIC_ONLY], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "called" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
