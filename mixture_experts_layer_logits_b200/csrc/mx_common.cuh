@@ -74,15 +74,21 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t bits)
     return max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
 }
 
-// Quantises 8 consecutive values of a block spread over 4 consecutive lanes (all 32
-// lanes take part).  `codes` gets 8 E4M3 bytes (E2M1: 8 nibbles in codes.x); returns
-// the block's scale code.
-template <bool E2M1>
-__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint2& codes)
+// The bits of the largest magnitude of 8 values, above every number's if one is a NaN.
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[8])
 {
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+    return m;
+}
+
+// Quantises 8 consecutive values of a block spread over 4 consecutive lanes (all 32
+// lanes take part); `m` is their max_bits.  `codes` gets 8 E4M3 bytes (E2M1: 8 nibbles in codes.x); returns
+// the block's scale code.
+template <bool E2M1>
+__device__ __forceinline__ uint32_t quantize8(const float (&v)[8], uint32_t m, uint2& codes)
+{
     m = quad_max(m);
     const uint32_t code = scale_code(m, E2M1 ? kEmaxE2M1 : kEmaxE4M3);
     if (code == kNanScale) {

@@ -43,7 +43,6 @@ namespace {
 using namespace mx;
 using gemm::named_bar_or;
 using gemm::named_bar_sync;
-using gemm::silu_mul;
 
 constexpr int kBM = 128;                  // weight rows of one CTA's tile
 constexpr int kATile = kBM * kBK;

@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(256)
     for (int u = 0; u < U; ++u) {
         const long c = c0 + 256 * u;
         uint2 q;
-        const uint32_t s = mx::quantize8<E2M1>(v[u], q);
+        const uint32_t s = mx::quantize8<E2M1>(v[u], mx::max_bits(v[u]), q);
         if (c >= chunks) continue;
         if constexpr (E2M1)
             reinterpret_cast<uint32_t*>(codes)[c] = q.x;
@@ -95,13 +95,12 @@ __device__ __forceinline__ float block_sum(float v, float* part)
 // One row per CTA.  h = x + residual rounded to bf16 (that is what the next layer
 // reads, so the norm is the norm of the stored sum), r = 1 / sqrt(mean(h^2) + eps),
 // n = (h * weight) * r: the product of two bf16 values is exact in fp32, so n carries
-// the rounding of r and of one product.  Sums are fp32.  h first takes the power of two that
-// brings the root mean square to 2^-14 .. 2^-13, and r the opposite one: h * weight is then out of
-// fp32's range only where n is, or is below bf16's.
-// kThreads, kMin: the most threads of a CTA, and CTAs an SM has to hold (2048 x 8192, C = 4: registers for
-// five CTAs of 256 threads 18.6 us, for six 17.1).
-template <int C, int kThreads, int kMin>
-__global__ void __launch_bounds__(kThreads, kMin)
+// the rounding of r and of one product.  Sums are fp32.  A row whose mean square is not
+// 2^-24 .. 2^24, or whose weights are so large that h * weight overflows, is done again: h first
+// takes the power of two that brings the root mean square to 2^-14 .. 2^-13, and r the opposite
+// one, so that h * weight is out of fp32's range only where n is, or is below bf16's.
+template <int C>
+__global__ void __launch_bounds__(1024, C <= 4 ? 2 : 1)
     rmsnorm_kernel(const uint4* x, const uint4* residual, const uint4* weight, int chunks, float inv_h, float eps,
                    uint4* sum, uint4* __restrict__ out, uint8_t* __restrict__ codes,
                    uint8_t* __restrict__ scales)
@@ -113,8 +112,9 @@ __global__ void __launch_bounds__(kThreads, kMin)
     uint4 h[C];
     float ss = 0.f;
     // Chunks whose loads are in flight together (8192 x 4096 with residual: one by one 51.1 us, two
-    // 46.6; 2048 x 8192: two 17.7, four 17.1).  At C = 8 the registers hold no more than two.
-    constexpr int kBatch = C < 8 ? C : 2;
+    // 46.6).  More of them take registers that CTAs need (32768 columns: 740 rows 42.2 us, with four
+    // and half the CTAs 40.5, but 296 rows 16.0 and 17.4).
+    constexpr int kBatch = C < 2 ? C : 2;
 #pragma unroll
     for (int i0 = 0; i0 < C; i0 += kBatch) {
         uint4 add[kBatch];
@@ -122,8 +122,8 @@ __global__ void __launch_bounds__(kThreads, kMin)
         for (int i = 0; i < kBatch; ++i) {
             const int c = threadIdx.x + (i0 + i) * blockDim.x;
             if (c >= chunks) continue;
-            h[i0 + i] = __ldcs(x + base + c);
-            if (residual) add[i] = __ldcs(residual + base + c);
+            h[i0 + i] = __ldcg(x + base + c);
+            if (residual) add[i] = __ldcg(residual + base + c);
         }
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
@@ -144,17 +144,50 @@ __global__ void __launch_bounds__(kThreads, kMin)
             for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
         }
     }
-    float m = fmaf(block_sum(ss, part), inv_h, eps), scale = 1.0f;
+    float m = fmaf(block_sum(ss, part), inv_h, eps);
+    auto put = [&](int c, bool live, const float (&v)[8]) {  // whether n's chunk c has a NaN or an infinity
+        if (live && out) out[base + c] = pack_bf16x8(v);
+        if (!codes) return mx::max_bits(v) >= 0x7F800000u;
+        uint2 q;
+        const uint32_t s = mx::quantize8<false>(v, mx::max_bits(v), q);
+        if (live) {
+            reinterpret_cast<uint2*>(codes)[base + c] = q;
+            if ((c & 3) == 0) scales[(base + c) >> 2] = (uint8_t)s;
+        }
+        return s == mx::kNanScale;
+    };
+    if (m >= 0x1p-24f && m <= 0x1p24f) {  // the same in every thread
+        const float r = 1.0f / sqrtf(m);
+        bool over = false;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const int c = threadIdx.x + i * blockDim.x;
+            const bool live = c < chunks;
+            float v[8] = {};
+            if (live) {
+                float w[8];
+                unpack_bf16x8(h[i], v);
+                unpack_bf16x8(__ldca(weight + c), w);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] = v[j] * w[j] * r;
+            }
+            over |= put(c, live, v);
+        }
+        if (!__any_sync(0xffffffffu, over)) return;
+    }
+
+    // Rows and weights of any size, from memory again: this costs the rows above no registers.
+    const uint4* const row = (residual ? sum : x) + base;
+    float scale = 1.0f;
     if (!(m >= 0x1p-100f && m < INFINITY)) {  // the same in every thread
         // Squares left the range of fp32, or they and eps lie so low that what underflowed would
         // count: once more for the row times a power of two (a NaN or an infinity stays one).
         scale = m < 1.0f ? 0x1p80f : 0x1p-80f;
         ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            if (threadIdx.x + i * blockDim.x >= chunks) continue;
+#pragma unroll 1
+        for (int c = threadIdx.x; c < chunks; c += blockDim.x) {
             float v[8];
-            unpack_bf16x8(h[i], v);
+            unpack_bf16x8(__ldcg(row + c), v);
 #pragma unroll
             for (int j = 0; j < 8; ++j) ss = fmaf(v[j] * scale, v[j] * scale, ss);
         }
@@ -165,34 +198,26 @@ __global__ void __launch_bounds__(kThreads, kMin)
     const int k = ((int)(__float_as_uint(m) >> 23 & 255) - 127 + 2) >> 1;
     const float down = scale * __uint_as_float((uint32_t)(127 - 13 - k) << 23);
     const float r = 1.0f / sqrtf(m) * __uint_as_float((uint32_t)(127 + 13 + k) << 23);
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < C; ++i) {
         const int c = threadIdx.x + i * blockDim.x;
         const bool live = c < chunks;
         float v[8] = {};
         if (live) {
             float w[8];
-            unpack_bf16x8(h[i], v);
+            unpack_bf16x8(__ldcg(row + c), v);
             unpack_bf16x8(__ldca(weight + c), w);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = (v[j] * down * w[j]) * r;
-            if (out) out[base + c] = pack_bf16x8(v);
+            for (int j = 0; j < 8; ++j) v[j] = v[j] * down * w[j] * r;
         }
-        if (codes) {
-            uint2 q;
-            const uint32_t s = mx::quantize8<false>(v, q);
-            if (live) {
-                reinterpret_cast<uint2*>(codes)[base + c] = q;
-                if ((c & 3) == 0) scales[(base + c) >> 2] = (uint8_t)s;
-            }
-        }
+        put(c, live, v);
     }
 }
 
-template <int C, int kThreads, int kMin>
+template <int C>
 cudaError_t launch_norm(const NormArgs& a, int threads, cudaStream_t st)
 {
-    return launch_pdl(rmsnorm_kernel<C, kThreads, kMin>, dim3(a.T), dim3(threads), 0, st,
+    return launch_pdl(rmsnorm_kernel<C>, dim3(a.T), dim3(threads), 0, st,
                       static_cast<const uint4*>(a.x), static_cast<const uint4*>(a.residual),
                       static_cast<const uint4*>(a.weight), a.H / 8, 1.0f / (float)a.H, a.eps,
                       static_cast<uint4*>(a.sum), static_cast<uint4*>(a.out), a.codes, a.scales);
@@ -203,19 +228,18 @@ cudaError_t launch_norm(const NormArgs& a, int threads, cudaStream_t st)
 cudaError_t launch_add_rmsnorm(const NormArgs& a, cudaStream_t st)
 {
     const int chunks = a.H / 8;
-    // Chunks of 8 elements: one per thread where there are few rows, and CTAs of 256 threads
-    // where rows fill the SMs several times (8192 x 4096 with residual and blocks: 48.5 us, 97% of
-    // the measured copy rate; with CTAs of 512 54.6 us, of 128 53.1 us).  CTAs of up to 1024 and of
-    // 256 threads at H = 7168: 64 rows 2.6 and 4.0 us, 592 7.0 and 9.7, 888 10.9 and 12.0, 1036
-    // 13.4 and 12.8, 4096 48.5 and 42.2; at H = 4096 they cross between 888 and 1036 rows too.
-    const int most = a.T >= 7 * device_sms() ? 256 : 1024;
-    const int c = (chunks + most - 1) / most;
-    const int cc = c <= 1 ? 1 : c <= 2 ? 2 : c <= 4 ? 4 : 8;
+    // Chunks of 8 elements a thread: one where there are few rows, two where rows fill the SMs several
+    // times and a CTA keeps 128 threads or more (with residual and blocks, one and two: 64 x 7168 2.9 and
+    // 3.1 us, 740 x 4096 6.1 and 6.5, 888 x 4096 6.8 and 7.0, 1184 x 4096 8.4 and 7.6, 1036 x 7168 13.4 and
+    // 11.0, 4096 x 7168 50.4 and 42.3), more only as 1024 threads cannot do without.
+    const bool many = a.T >= 7 * device_sms() && chunks > 256;
+    const int c = max((chunks + 1023) / 1024, many ? 2 : 1);
+    const int cc = c <= 2 ? c : c <= 4 ? 4 : 8;
     const int threads = ((chunks + cc - 1) / cc + 31) & ~31;
-    if (cc == 1) return launch_norm<1, 1024, 2>(a, threads, st);
-    if (cc == 2) return launch_norm<2, 1024, 2>(a, threads, st);
-    if (cc == 4) return most == 256 ? launch_norm<4, 256, 6>(a, threads, st) : launch_norm<4, 1024, 1>(a, threads, st);
-    return launch_norm<8, 1024, 1>(a, threads > 1024 ? 1024 : threads, st);
+    if (cc == 1) return launch_norm<1>(a, threads, st);
+    if (cc == 2) return launch_norm<2>(a, threads, st);
+    if (cc == 4) return launch_norm<4>(a, threads, st);
+    return launch_norm<8>(a, threads, st);
 }
 
 template <bool E2M1, typename Src, int U>

@@ -92,6 +92,7 @@ def check_norm(x, w, eps, residual=None):
     err = err + 2.0 ** -135 * (1 + w.to(ref.F64).abs())
     ref.assert_within(out, n, err + ref.BF16_HALF_STEP * (n.abs() + err) + 2.0 ** -134, "out")
     ref.assert_within(ref.decode(codes, scales, "e4m3"), ref.mx(n), ref.mx_shift(n, err), "codes")
+    assert torch.equal(moe.moe_add_rmsnorm(x, w, eps, residual=residual)[1], out)   # without the blocks
     return out
 
 
@@ -136,13 +137,13 @@ def test_norm_of_few_huge_or_tiny_elements(T):
 
 
 @pytest.mark.parametrize("size", [-50, -10, 0, 40, 70, 110])
-def test_norm_with_weights_of_any_size(size):
+@pytest.mark.parametrize("T,H", [(3, 512), (1100, 4096), (2, 20480), (1, 65536)])
+def test_norm_with_weights_of_any_size(T, H, size):
     """The product of a row and its weights may pass fp32's range where the norm does not."""
-    H = 512
-    x = torch.ldexp(randn(3, H, g=gen(73)).to(BF16), torch.tensor(size, device="cuda"))
-    we = torch.tensor([-120, -90, -60, 0, 60, 90, 110, 124], device="cuda").repeat_interleave(64)
+    x = torch.ldexp(randn(T, H, g=gen(73)).to(BF16), torch.tensor(size, device="cuda"))
+    we = torch.tensor([-120, -90, -60, 0, 60, 90, 110, 124], device="cuda").repeat_interleave(64).repeat(H // 512)
     w = torch.ldexp(1 + 0.3 * randn(H, g=gen(74)).clamp(-2, 2), we).to(BF16)
-    check_norm(x, w, 1e-30)
+    check_norm(x, w, 1e-30, residual=torch.zeros_like(x) if H == 4096 else None)
 
 
 def test_norm_of_zero_rows_without_eps_is_nan():
