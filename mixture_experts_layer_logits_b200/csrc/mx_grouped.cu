@@ -744,6 +744,8 @@ cudaError_t launch_nt(MxArgs g, cudaStream_t st)
 // wider tile than needed costs little (E = 32, N = K = 2048, 2 rows an expert: NT = 16 15.9 us,
 // 64 16.1, 128 16.3, 208 18.5); beyond 64 the average decides: 64 rows an expert 128 19.8 us, 208
 // 22.4; 128 rows 22.4 and 25.2; 160 rows 30.0 and 26.1; 256 rows 36.4 and 39.0; 400 rows 60.3 and 48.5.
+// From 209 to 256 rows an expert both widths cut a group in two and 128 is the faster; the rule
+// does not tell these from the rest above 128.
 template <int MODE>
 cudaError_t launch_mode(const MxArgs& g, int most, cudaStream_t st)
 {
